@@ -374,11 +374,195 @@ moe_status moe_selftest_wait_timeout(moe_handle* handle, int microseconds, void*
  * MOE_ERR_CUDA on a launch or copy failure. */
 moe_status moe_selftest_nvfp4_convert(unsigned long long* mismatches_host, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Stand-alone operators.  They need no handle: weights, workspaces and outputs
+ * are the caller's device memory, each call runs on `stream` of the current
+ * device, asynchronously, allocates nothing and may be captured into a graph.
+ * Calls that overlap must not share outputs or a workspace.  Arguments are
+ * checked on the host before any launch; strides (ld...) count elements.  A
+ * call with no rows returns MOE_OK without a launch unless stated otherwise.
+ * What their kernels find wrong on the device is reported, and cleared, by
+ * moe_sync(NULL, stream) for the current device.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+
+/* Top-k routing of given router logits (moe_forward's selection on its own,
+ * with softmax scores, weights that need not be renormalised, and masks):
+ *   s      = sigmoid(l)  or  softmax(l) over the row's experts; evaluated in
+ *            fp64 and rounded once to fp32
+ *   choice = s + bias                          (fp32; selection only)
+ *   idx    = top_k eligible experts by (choice descending, expert ascending);
+ *            n_group > 1: only the topk_group best groups, as in moe_config
+ *   w      = s[idx] / (sum s[idx] + 1e-20) * scale     (renorm != 0; the sum in
+ *            slot order)  or  s[idx] * scale
+ * A logit of -inf or NaN, or a choice score that is -inf or NaN through its
+ * bias, takes the expert out of the row (softmax: a -inf or NaN logit has no
+ * part in the sum; +inf logits share the row equally).  A slot that no eligible
+ * expert is left for takes the lowest expert not yet taken and weight 0, so a
+ * row always names top_k different experts.  For an fp32 layer's logits
+ * (moe_get_router_logits) of magnitude up to 80 the results are moe_forward's
+ * bit for bit.
+ *   logits [T, n_experts] dtype, row stride ld >= n_experts; bias [n_experts]
+ *   fp32 or NULL; topk_idx, topk_w [T, top_k].  n_experts <= 1024, top_k <= 64
+ *   and n_group <= 64 (MOE_ERR_UNSUPPORTED beyond); group rules as moe_config. */
+moe_status moe_route_topk(const void* logits, moe_dtype dtype, int64_t ld, const float* bias,
+                          int T, int n_experts, int top_k, moe_score score, int n_group,
+                          int topk_group, int renorm, float scale, int32_t* topk_idx,
+                          float* topk_w, void* stream);
+
+/* Gradient of moe_route_topk's weights: dlogits [T, n_experts] (dtype, row
+ * stride ldd, every element written) from dw [T, top_k] fp32 and the forward's
+ * logits, topk_idx and topk_w.  The selection itself has no gradient; a slot of
+ * weight 0 gives none.  Indices outside [0, n_experts) are skipped; a row's
+ * indices are distinct, as moe_route_topk writes them.  dlogits may not
+ * overlap logits. */
+moe_status moe_route_topk_backward(const void* logits, moe_dtype dtype, int64_t ld,
+                                   const int32_t* topk_idx, const float* topk_w, const float* dw,
+                                   int T, int n_experts, int top_k, moe_score score, int renorm,
+                                   float scale, void* dlogits, int64_t ldd, void* stream);
+
+/* Grouping of the pairs p = t*top_k + j by expert (what moe_get_routing reports
+ * for a layer), from any topk_idx [T, top_k]:
+ *   counts [n_experts], offsets [n_experts + 1], perm [T*top_k] pair ids by
+ *   (expert, pair), pos [T*top_k] the place of a pair in perm
+ * The same expert may occur twice in a row.  An index outside [0, n_experts)
+ * joins no group (pos = -1), the end of perm it leaves free is -1, and
+ * moe_sync(NULL, stream) then reports MOE_ERR_DEVICE_CHECK.  T = 0 writes zero
+ * counts and offsets.  workspace: moe_route_group_workspace(..) bytes, 16-byte
+ * aligned; T * top_k < 2^31. */
+size_t moe_route_group_workspace(int T, int top_k, int n_experts);
+moe_status moe_route_group(const int32_t* topk_idx, int T, int top_k, int n_experts,
+                           int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* pos,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* What stands between two blocks of the residual stream, x being the stream, y
+ * the block's output:
+ *   n = y * ry * post_weight,  ry = 1 / sqrt(mean(y^2) + eps)   (n = y if NULL)
+ *   r = residual_scale * x + gate * n                           rounded to dtype
+ *   h = r * rr * pre_weight,   rr = 1 / sqrt(mean(r^2) + eps)   (none if NULL)
+ * r is the new stream, h the next block's input; h reads r as it is stored.
+ * Sums and statistics are fp32.  gate, in dtype:
+ *   MOE_GATE_NONE 1;  MOE_GATE_CHANNEL [D];  MOE_GATE_TOKEN one element a row,
+ *   stride ldg;  MOE_GATE_FULL [T, D], row stride ldg
+ * Rows have D contiguous elements and start at multiples of their stride; every
+ * pointer and every stride in bytes is a multiple of 16 (a token gate's need
+ * not be).  D is a multiple of 8, at most 16384 (MOE_ERR_UNSUPPORTED beyond).
+ * r may be x, and h may be y (same stride); nothing else may overlap.
+ * moe_norm_residual reads x, y, post_weight, pre_weight, gate and writes r, h
+ * (with pre_weight) and, where the pointers are given, rstd_y (with
+ * post_weight) and rstd_r (with pre_weight), [T] fp32.
+ *
+ * moe_norm_residual_backward reads y, r, the weights, the gate, rstd_y, rstd_r
+ * (as the forward wrote them), dr (gradient of r, NULL for zero) and dh
+ * (gradient of h, with pre_weight), and writes dx, dy (dtype; dx may be dr, dy
+ * may be dh), dpost_weight, dpre_weight [D] fp32 (with the weights) and dgate:
+ * [D] fp32, [T] fp32 or [T, D] dtype (row stride lddg) by the gate's kind.
+ * Sums over rows are taken in a fixed order.  T = 0 writes zero sums.
+ * workspace: moe_norm_residual_workspace(T, D) bytes, 16-byte aligned. */
+typedef enum {
+  MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3
+} moe_gate;
+
+typedef struct {
+  int T, D;
+  moe_dtype dtype;
+  moe_gate gate_kind;
+  float residual_scale, eps;
+  const void* x;          int64_t ldx;
+  const void* y;          int64_t ldy;
+  const void* post_weight;
+  const void* pre_weight;
+  const void* gate;       int64_t ldg;
+  void* r;                int64_t ldr;
+  void* h;                int64_t ldh;
+  float* rstd_y;
+  float* rstd_r;
+  const void* dr;         int64_t lddr;     /* backward only, from here on */
+  const void* dh;         int64_t lddh;
+  void* dx;               int64_t lddx;
+  void* dy;               int64_t lddy;
+  float* dpost_weight;
+  float* dpre_weight;
+  void* dgate;            int64_t lddg;
+} moe_norm_args;
+
+moe_status moe_norm_residual(const moe_norm_args* args, void* stream);
+size_t moe_norm_residual_workspace(int T, int D);
+moe_status moe_norm_residual_backward(const moe_norm_args* args, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Quantisation to E4M3 codes with an fp32 scale for each block of 128:
+ *   amax = max(|v| over the block, 2^-100);  scale = amax / 448;
+ *   code = E4M3(v * (448 / amax))   fp32 operations, nearest even, saturating
+ * so that value(code) * scale stands for v.  A NaN gives a NaN code; an
+ * infinite element makes its whole block NaN.  Elements past the matrix count
+ * as zeros in their block and have no codes.
+ * Codes lie in rows of ldc bytes, ldc a multiple of 16, 16-byte aligned (what
+ * moe_gemm_fp8 reads); bytes between a row's codes and ldc are not written.
+ *
+ * moe_quantize_fp8: blocks of 1 x 128 along K.  x [x_rows, K] dtype, row stride
+ * ldx; codes [rows, ldc]; scales [ceil(K/128)] rows of lds >= rows floats, one
+ * row for each K block.  perm == NULL: rows == x_rows.  Otherwise output row r
+ * is the input row perm[r] / k (pairs grouped by moe_route_group); a perm
+ * entry that names no row gives a row of zeros.  relu2 != 0 quantises
+ * max(x, 0)^2 (the experts' activation), computed in fp32.
+ * moe_quantize_fp8_t: the same for the transpose: blocks of 128 x 1 down the
+ * rows of x [rows, K]; codes [K, ldc >= rows], scales [ceil(rows/128)] rows of
+ * lds >= K floats.
+ * moe_quantize_fp8_weight: n_mat matrices [N, K] (N*ldw elements apart), blocks
+ * of 128 x 128; codes [n_mat, N, ldc], scales [n_mat, ceil(N/128),
+ * ceil(K/128)].  With codes_t and scales_t (both or neither) also the
+ * transposes: [n_mat, K, ldct], [n_mat, ceil(K/128), ceil(N/128)]. */
+moe_status moe_quantize_fp8(const void* x, moe_dtype dtype, int x_rows, int K, int64_t ldx,
+                            const int32_t* perm, int rows, int k, int relu2, uint8_t* codes,
+                            int64_t ldc, float* scales, int64_t lds, void* stream);
+moe_status moe_quantize_fp8_t(const void* x, moe_dtype dtype, int rows, int K, int64_t ldx,
+                              uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                              void* stream);
+moe_status moe_quantize_fp8_weight(const void* w, moe_dtype dtype, int n_mat, int N, int K,
+                                   int64_t ldw, uint8_t* codes, int64_t ldc, float* scales,
+                                   uint8_t* codes_t, int64_t ldct, float* scales_t, void* stream);
+
+/* out[m, n] = sum_k A[m, k] * B[n, k] of E4M3 operands:
+ *   A  codes a [M, lda], scales a_scales: ceil(K/128) rows of lda_scales >= M
+ *      floats (moe_quantize_fp8's)
+ *   B  ldb_scales == 0: weights, codes b [N, ldb], a scale for each 128 x 128
+ *      block (moe_quantize_fp8_weight's); ldb_scales >= N: a second operand of
+ *      A's kind, b_scales ceil(K/128) rows of ldb_scales floats
+ * Each block of 128 products is summed by the tensor core, then scaled and
+ * added in fp32 in the order of the blocks; out is rounded once to out_dtype.
+ * The three products of a linear layer y = x W^T, all sums along K:
+ *   y:  A = x, B = W;   dx: A = dy, B = W transposed;
+ *   dW: A = dy transposed, B = x transposed (ldb_scales >= N)
+ * Grouped (offsets != NULL; weights only): rows [offsets[g], offsets[g+1]) of A
+ * and out belong to group g of n_groups <= 1024, b is [n_groups, N, ldb] and
+ * b_scales [n_groups, ceil(N/128), ceil(K/128)].  offsets [n_groups + 1] int32,
+ * device, ascending, within [0, M] (others are clamped to that).  Rows of out
+ * outside every group are not written.
+ * out [M, N], row stride ldo >= N.  Codes as moe_quantize_fp8 lays them out.
+ * A device wait that runs out is reported by moe_sync(NULL, stream) as
+ * MOE_ERR_TIMEOUT. */
+typedef struct {
+  int M, N, K;
+  int n_groups;                  /* grouped only */
+  const int32_t* offsets;
+  const uint8_t* a;        int64_t lda;
+  const float* a_scales;   int64_t lda_scales;
+  const uint8_t* b;        int64_t ldb;
+  const float* b_scales;   int64_t ldb_scales;
+  void* out;               int64_t ldo;
+  moe_dtype out_dtype;
+} moe_fp8_gemm;
+
+moe_status moe_gemm_fp8(const moe_fp8_gemm* args, void* stream);
+
 /* Drain `stream` and report (then clear) the handle's device error word:
  * MOE_ERR_TIMEOUT when a bounded wait gave up, MOE_ERR_DEVICE_CHECK for the
- * other device-side checks.  With handle == NULL the word reported is
- * moe_route_noalloc's, in its fixed array on the current device (MOE_OK when
- * no such call ran there). */
+ * other device-side checks.  With handle == NULL the words reported are those
+ * of the calls without a handle on the current device: moe_route_noalloc's, in
+ * its fixed array, and the stand-alone operators' (MOE_OK when no such call ran
+ * there). */
 moe_status moe_sync(moe_handle* handle, void* stream);
 
 /* Free everything moe_init allocated.  NULL is ignored. */

@@ -47,6 +47,41 @@ class moe_weights(ctypes.Structure):
                 ("weights_on_device", ctypes.c_int)]
 
 
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+SCORE = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
+
+
+class moe_norm_args(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("gate_kind", ctypes.c_int), ("residual_scale", ctypes.c_float),
+                ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("rstd_y", ctypes.c_void_p), ("rstd_r", ctypes.c_void_p),
+                ("dr", ctypes.c_void_p), ("lddr", ctypes.c_int64),
+                ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dpost_weight", ctypes.c_void_p), ("dpre_weight", ctypes.c_void_p),
+                ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64)]
+
+
+class moe_fp8_gemm(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("n_groups", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("a_scales", ctypes.c_void_p), ("lda_scales", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+                ("b_scales", ctypes.c_void_p), ("ldb_scales", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status, what):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -54,6 +89,7 @@ class MoeError(RuntimeError):
 
 
 _vp, _i, _p = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER
+_i64 = ctypes.c_int64
 # (name, restype, argtypes) of every entry point declared in include/latentmoe.h
 SIGNATURES = [
     ("moe_init", _i, [_p(_vp), _p(moe_config), _p(moe_weights), _vp]),
@@ -72,6 +108,20 @@ SIGNATURES = [
     ("moe_route_noalloc", _i, [_vp, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _i,
                                _vp, _vp, _vp]),
     ("moe_quantize_nvfp4", _i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    ("moe_route_topk", _i, [_vp, _i, _i64, _vp, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float,
+                            _vp, _vp, _vp]),
+    ("moe_route_topk_backward", _i, [_vp, _i, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                     ctypes.c_float, _vp, _i64, _vp]),
+    ("moe_route_group_workspace", ctypes.c_size_t, [_i, _i, _i]),
+    ("moe_route_group", _i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    ("moe_norm_residual", _i, [_p(moe_norm_args), _vp]),
+    ("moe_norm_residual_workspace", ctypes.c_size_t, [_i, _i]),
+    ("moe_norm_residual_backward", _i, [_p(moe_norm_args), _vp, ctypes.c_size_t, _vp]),
+    ("moe_quantize_fp8", _i, [_vp, _i, _i, _i, _i64, _vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
+    ("moe_quantize_fp8_t", _i, [_vp, _i, _i, _i, _i64, _vp, _i64, _vp, _i64, _vp]),
+    ("moe_quantize_fp8_weight", _i, [_vp, _i, _i, _i, _i, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                                     _vp]),
+    ("moe_gemm_fp8", _i, [_p(moe_fp8_gemm), _vp]),
     ("moe_get_router_stats", _i, [_vp, _p(ctypes.c_ulonglong), _vp]),
     ("moe_selftest_wait_timeout", _i, [_vp, _i, _vp]),
     ("moe_selftest_nvfp4_convert", _i, [_vp, _vp]),
@@ -191,6 +241,64 @@ def moe_route_noalloc(hidden, w_gate, gate_bias, T, d_model, n_experts, top_k, r
 def moe_quantize_nvfp4(w, dtype, n_mat, rows, K, codes, scales, gscale, stream):
     _check(_lib.moe_quantize_nvfp4(w, dtype, n_mat, rows, K, codes, scales, gscale, stream),
            "moe_quantize_nvfp4")
+
+
+def moe_route_topk(logits, dtype, ld, bias, T, n_experts, top_k, score, n_group, topk_group,
+                   renorm, scale, topk_idx, topk_w, stream):
+    _check(_lib.moe_route_topk(logits, dtype, ld, bias, T, n_experts, top_k, score, n_group,
+                               topk_group, renorm, scale, topk_idx, topk_w, stream),
+           "moe_route_topk")
+
+
+def moe_route_topk_backward(logits, dtype, ld, topk_idx, topk_w, dw, T, n_experts, top_k, score,
+                            renorm, scale, dlogits, ldd, stream):
+    _check(_lib.moe_route_topk_backward(logits, dtype, ld, topk_idx, topk_w, dw, T, n_experts,
+                                        top_k, score, renorm, scale, dlogits, ldd, stream),
+           "moe_route_topk_backward")
+
+
+def moe_route_group_workspace(T, top_k, n_experts) -> int:
+    return _lib.moe_route_group_workspace(T, top_k, n_experts)
+
+
+def moe_route_group(topk_idx, T, top_k, n_experts, counts, offsets, perm, pos, workspace,
+                    workspace_bytes, stream):
+    _check(_lib.moe_route_group(topk_idx, T, top_k, n_experts, counts, offsets, perm, pos,
+                                workspace, workspace_bytes, stream), "moe_route_group")
+
+
+def moe_norm_residual(args: moe_norm_args, stream):
+    _check(_lib.moe_norm_residual(ctypes.byref(args), stream), "moe_norm_residual")
+
+
+def moe_norm_residual_workspace(T, D) -> int:
+    return _lib.moe_norm_residual_workspace(T, D)
+
+
+def moe_norm_residual_backward(args: moe_norm_args, workspace, workspace_bytes, stream):
+    _check(_lib.moe_norm_residual_backward(ctypes.byref(args), workspace, workspace_bytes, stream),
+           "moe_norm_residual_backward")
+
+
+def moe_quantize_fp8(x, dtype, x_rows, K, ldx, perm, rows, k, relu2, codes, ldc, scales, lds,
+                     stream):
+    _check(_lib.moe_quantize_fp8(x, dtype, x_rows, K, ldx, perm, rows, k, relu2, codes, ldc,
+                                 scales, lds, stream), "moe_quantize_fp8")
+
+
+def moe_quantize_fp8_t(x, dtype, rows, K, ldx, codes, ldc, scales, lds, stream):
+    _check(_lib.moe_quantize_fp8_t(x, dtype, rows, K, ldx, codes, ldc, scales, lds, stream),
+           "moe_quantize_fp8_t")
+
+
+def moe_quantize_fp8_weight(w, dtype, n_mat, N, K, ldw, codes, ldc, scales, codes_t, ldct,
+                            scales_t, stream):
+    _check(_lib.moe_quantize_fp8_weight(w, dtype, n_mat, N, K, ldw, codes, ldc, scales, codes_t,
+                                        ldct, scales_t, stream), "moe_quantize_fp8_weight")
+
+
+def moe_gemm_fp8(args: moe_fp8_gemm, stream):
+    _check(_lib.moe_gemm_fp8(ctypes.byref(args), stream), "moe_gemm_fp8")
 
 
 def moe_get_router_stats(h, stream) -> int:

@@ -1207,8 +1207,12 @@ moe_status moe_sync(moe_handle* h, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
   if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
   int word = 0;
-  if (!h) {                      // the error word of moe_route_noalloc's fixed array
-    if (noalloc_take_error(&word) != cudaSuccess) return MOE_ERR_CUDA;
+  if (!h) {                      // the calls without a handle: fixed array, operators
+    int group = 0, gemm = 0;
+    if (noalloc_take_error(&word) != cudaSuccess || route_group_take_error(&group) != cudaSuccess ||
+        fp8_gemm_take_error(&gemm) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    word |= group | gemm;
   } else {
     if (cudaMemcpy(&word, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
       return MOE_ERR_CUDA;

@@ -68,6 +68,6 @@ __device__ __forceinline__ float relu2(float v) {
   return r * r;
 }
 
-inline int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
+__host__ __device__ inline int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
 
 }  // namespace lmoe

@@ -249,4 +249,45 @@ void launch_gather_rows_f16(const void* z, const int32_t* perm, void* zp, long P
 cudaError_t launch_pow2_scale(const void* z, long n, unsigned* amax, float* mul2, cudaStream_t st);
 void launch_gather_rows(const void* z, const int32_t* perm, void* zp, long P, int k, int L,
                         cudaStream_t st);
+// 8-bit codes [rows][K], rows of `pitch` bytes (a multiple of 16), 128-byte x
+// box_rows boxes, 128-byte swizzle
+bool make_tmap_codes(CUtensorMap* map, const void* base, long rows, int K, long pitch,
+                     int box_rows);
+}  // namespace lmoe
+
+// Stand-alone operators (ops_api.cu checks the arguments)
+namespace lmoe {
+// route_ops.cu
+cudaError_t launch_route_topk(const void* logits, moe_dtype dt, long ld, const float* bias, int T,
+                              int E, int k, moe_score score, int n_group, int topk_group,
+                              int renorm, float scale, int32_t* idx, float* w, cudaStream_t st);
+cudaError_t launch_route_topk_bwd(const void* logits, moe_dtype dt, long ld, const int32_t* idx,
+                                  const float* w, const float* dw, int T, int E, int k,
+                                  moe_score score, int renorm, float scale, void* dl, long ldd,
+                                  cudaStream_t st);
+size_t route_group_workspace(long P, int E);
+cudaError_t launch_route_group(const int32_t* idx, long P, int E, int32_t* counts,
+                               int32_t* offsets, int32_t* perm, int32_t* pos, void* ws,
+                               cudaStream_t st);
+// norm_ops.cu
+size_t norm_bwd_workspace(int T, int D);
+cudaError_t launch_norm_fwd(const moe_norm_args& a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const moe_norm_args& a, void* ws, cudaStream_t st);
+// fp8_quant.cu
+cudaError_t launch_quantize_fp8_rows(const void* x, moe_dtype dt, int rows, int K, long ldx,
+                                     const int32_t* perm, int k, int x_rows, int relu2,
+                                     uint8_t* codes, long ldc, float* scales, long lds,
+                                     cudaStream_t st);
+cudaError_t launch_quantize_fp8_cols(const void* x, moe_dtype dt, int rows, int K, long ldx,
+                                     uint8_t* codes, long ldc, float* scales, long lds,
+                                     cudaStream_t st);
+cudaError_t launch_quantize_fp8_weight(const void* w, moe_dtype dt, int n_mat, int N, int K,
+                                       long ldx, uint8_t* codes, long ldc, float* scales,
+                                       uint8_t* codes_t, long ldct, float* scales_t,
+                                       cudaStream_t st);
+// umma_fp8.cu
+cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st);
+// the device error words of the calls without a handle: read, then cleared
+cudaError_t route_group_take_error(int* word);
+cudaError_t fp8_gemm_take_error(int* word);
 }  // namespace lmoe

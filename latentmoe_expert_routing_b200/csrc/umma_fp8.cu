@@ -1,0 +1,534 @@
+// Products of E4M3 operands with one fp32 scale for each block of 128 along K:
+//   out[m, n] = sum_kb sa[kb][m] sb[kb][n] sum_{k in block kb} a[m, k] b[n, k]
+// a: activations (a scale per row and K block).  b: weights with a scale per
+// 128 x 128 block, or a second matrix of the first kind (the weight gradient).
+// Rows of a may be grouped, group g taking weight matrix g.
+//
+// The inner sum of 128 products is one tcgen05 accumulation (kind::f8f6f4, four
+// K = 32 MMAs) into one of two TMEM buffers.  The tensor core cannot apply an
+// fp32 scale, so "promoting" warps read every 128-K partial back and add
+// scale * partial to fp32 registers while the tensor core fills the other
+// buffer.  Per 128-K step of a 128 x 256 tile the MMAs take 512 cycles and the
+// 32768 FMAs of the promotion 256, so the promotion hides behind the products.
+//
+// Two forms of the tile:
+//   wide  MMA rows = 128 activation rows, MMA columns = 256 weight rows; a
+//         thread owns one activation row, and its scale product is one number
+//         for each 128 columns (per column in the weight gradient).
+//   tall  MMA rows = 128 weight rows, MMA columns = 16..128 activation rows:
+//         for few rows, where streaming the weights is the work.  Two CTAs per
+//         SM keep more loads in flight; when the tiles cannot fill the GPU, K
+//         is split over the CTAs of a cluster, which add their sums in rank
+//         order through distributed shared memory (no atomics: one order).
+//
+// Roles: one producer warp (TMA tiles by lane 0; the scales by cp.async from
+// all lanes, in a ring of their own because the promotion reads them after the
+// tile's stage is free again), one MMA thread, 4 or 16 promoting warps.  Every
+// wait is bounded; one that runs out sets DEV_ERR_TIMEOUT and unwinds.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "pair_sm100.cuh"
+#include "sm100.cuh"
+
+namespace lmoe {
+
+namespace {
+
+using namespace sm100;
+
+__device__ int g_fp8_err;
+
+constexpr int kRowsP = 128;               // MMA rows of a tile
+constexpr int kKB = 128;                  // K elements (bytes) per step
+constexpr int kPBytes = kRowsP * kKB;
+constexpr int kScaleRing = 8;
+constexpr int kMaxGroups = 1024;
+
+enum Form { WIDE_BLOCK = 0, WIDE_ROW = 1, TALL = 2 };
+
+struct Fp8Args {
+  const float* sa;          // [KB][ldsa]
+  long ldsa;
+  const float* sb;          // block scales [G][NB][KB], or [KB][ldsb]
+  long ldsb;
+  const int32_t* offsets;   // [G + 1] or NULL
+  void* out;
+  long ldo;
+  int M, N, KB, G, NB;
+  int split;                // CTAs per tile (cluster size), TALL only
+  int vec;                  // out rows take 16-byte stores
+};
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate));
+}
+
+// fp32 accumulator, E4M3 operands (format 0), both K-major
+__device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// 4 bytes to shared memory, zeros when !ok
+__device__ __forceinline__ void cp_async4(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// the barrier gets this thread's arrival once its cp.async so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int NT, int FORM>
+struct Cfg {
+  static constexpr bool kTall = FORM == TALL;
+  static constexpr int kQBytes = NT * kKB;
+  static constexpr int kStageBytes = kPBytes + kQBytes;
+  static constexpr int kStages = kTall ? (NT <= 32 ? 5 : NT == 64 ? 4 : 3) : 4;
+  static constexpr int kWarps = kTall ? 4 : 16;                 // promoting warps
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kCols = NT * 4 / kWarps;                 // columns per promoting thread
+  static constexpr int kQScales = FORM == WIDE_BLOCK ? 4 : NT;  // column scales per step
+  static constexpr int kScaleFloats = kRowsP + kQScales;
+  static constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kScaleOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
+  static constexpr int kTableOffset = kBarOffset + 512;
+  static constexpr int bytes(int groups) {         // groups: 0 for a plain product
+    return kTableOffset + (groups ? 2 * (groups + 1) * 4 : 0) + 1024;
+  }
+};
+
+struct Tile {
+  int grp;
+  int m0, rows;      // activation rows [m0, m0 + rows)
+  int n0, cols;      // weight rows [n0, n0 + cols) of the group's matrix
+};
+
+// Tile t: the weight blocks of a group run fastest over its row tiles, so that
+// the CTAs in flight share weight blocks and row tiles through L2.
+template <int NT, int FORM>
+__device__ __forceinline__ bool decode(const Fp8Args& a, const int* s_tiles, const int* s_off, int t,
+                                       Tile& o) {
+  constexpr int RM = FORM == TALL ? NT : kRowsP, RN = FORM == TALL ? kRowsP : NT;
+  const int nn = (a.N + RN - 1) / RN;
+  int lo = 0, base = 0, cnt = a.M;
+  if (a.offsets) {
+    int hi = a.G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_tiles[mid] <= t) lo = mid; else hi = mid;
+    }
+    base = s_off[lo];
+    cnt = s_off[lo + 1] - base;
+    t -= s_tiles[lo];
+  }
+  const int nm = (cnt + RM - 1) / RM;
+  if (nm <= 0) return false;
+  int im, in;
+  if (FORM == TALL) {
+    in = t / nm; im = t - in * nm;
+  } else {
+    // bands of 8 row tiles: a wave's tiles form a block, not a strip
+    const int band = t / (8 * nn), left = nm - band * 8, h = left < 8 ? left : 8;
+    const int u = t - band * 8 * nn;
+    in = u / h; im = band * 8 + u - in * h;
+  }
+  if (in >= nn || im >= nm) return false;
+  o.grp = lo;
+  o.m0 = base + im * RM;
+  o.rows = min(RM, cnt - im * RM);
+  o.n0 = in * RN;
+  o.cols = min(RN, a.N - in * RN);
+  return true;
+}
+
+// tile offsets [G + 1] and row offsets [G + 1] of the groups.  Offsets are
+// clamped to [0, M] and made ascending, so that whatever the caller's array
+// holds, every tile lies inside a, b and out.
+template <int RM, int RN>
+__device__ void load_groups(const Fp8Args& a, int* s_tiles, int* s_off) {
+  if (!a.offsets) return;
+  const int nn = (a.N + RN - 1) / RN;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int top = 0, tiles = 0;
+    for (int g0 = 0; g0 <= a.G; g0 += 32) {
+      const int g = g0 + lane;
+      int v = g <= a.G ? min(max(a.offsets[g], 0), a.M) : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v = max(v, y);
+      }
+      v = max(v, top);
+      int prev = __shfl_up_sync(0xffffffffu, v, 1);
+      if (lane == 0) prev = g0 == 0 ? v : top;
+      // tiles of group g - 1 lie before tile offset g
+      int n = g <= a.G && g > 0 ? (v - prev + RM - 1) / RM * nn : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, n, off);
+        if (lane >= off) n += y;
+      }
+      if (g <= a.G) { s_off[g] = v; s_tiles[g] = tiles + n; }
+      tiles += __shfl_sync(0xffffffffu, n, 31);
+      top = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+}
+
+template <int NT, int FORM, typename TO>
+__global__ void __launch_bounds__(Cfg<NT, FORM>::kThreads, FORM == TALL ? 2 : 1)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                const Fp8Args a, const int n_tiles) {
+  using C = Cfg<NT, FORM>;
+  constexpr bool kTall = FORM == TALL;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOffset);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* sfull = empty + C::kStages;
+  uint64_t* sempty = sfull + kScaleRing;
+  uint64_t* tfull = sempty + kScaleRing;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_tiles = reinterpret_cast<int*>(smem + C::kTableOffset);
+  int* s_off = s_tiles + a.G + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kTall && a.split > 1 ? pair2::cluster_rank() : 0u;
+  const int split = kTall ? a.split : 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < kScaleRing; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], C::kWarps); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], C::kWarps); }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&amap);
+    tma_prefetch_desc(&bmap);
+  }
+  if (warp == 1) { tmem_alloc(tmem_slot, C::kTmemCols); tmem_relinquish(); }
+  load_groups<kTall ? NT : kRowsP, kTall ? kRowsP : NT>(a, s_tiles, s_off);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int ntiles = a.offsets ? s_tiles[a.G] : n_tiles;
+  const int kb0 = (int)((long)a.KB * rank / split), kb1 = (int)((long)a.KB * (rank + 1) / split);
+  const int first = blockIdx.x / split, step = gridDim.x / split;
+
+  auto fail = [&]() {
+    atomicOr(&g_fp8_err, DEV_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+      Tile ti;
+      if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
+      const CUtensorMap* pm = kTall ? &bmap : &amap;
+      const CUtensorMap* qm = kTall ? &amap : &bmap;
+      const int brow = ti.grp * a.N + ti.n0;
+      const int prow = kTall ? brow : ti.m0, qrow = kTall ? ti.m0 : brow;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t st = it % C::kStages, ss = it % kScaleRing;
+        ok = mbar_wait(&empty[st], ((it / C::kStages) & 1) ^ 1) &&
+             mbar_wait(&sempty[ss], ((it / kScaleRing) & 1) ^ 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+          uint8_t* sp = smem + st * C::kStageBytes;
+          tma_load_2d(sp, pm, &full[st], kb * kKB, prow);
+          tma_load_2d(sp + kPBytes, qm, &full[st], kb * kKB, qrow);
+        }
+        // scales: rows first, columns behind them
+        float* sc = s_scale + ss * C::kScaleFloats;
+        const float* sa = a.sa + (size_t)kb * a.ldsa + ti.m0;
+        if (kTall) {
+          const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB + kb;
+          if (lane == 0) cp_async4(sc, sb, true);
+          for (int i = lane; i < NT; i += 32) cp_async4(sc + kRowsP + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
+        } else {
+          for (int i = lane; i < kRowsP; i += 32) cp_async4(sc + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
+          if (FORM == WIDE_BLOCK) {
+            if (lane < NT / 128 && lane * 128 < ti.cols)
+              cp_async4(sc + kRowsP + lane, a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128 + lane) * a.KB + kb, true);
+          } else {
+            const float* sb = a.sb + (size_t)kb * a.ldsb + ti.n0;
+            for (int i = lane; i < NT; i += 32) cp_async4(sc + kRowsP + i, sb + (i < ti.cols ? i : 0), i < ti.cols);
+          }
+        }
+        cp_async_arrive(&sfull[ss]);
+      }
+    }
+    // nothing may be in flight into this CTA's memory when it ends
+    const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+    for (uint32_t j = 0; j < n && ok; ++j) {
+      const uint32_t i = it - 1 - j;
+      if (!mbar_wait(&empty[i % C::kStages], (i / C::kStages) & 1)) { ok = false; fail(); }
+    }
+    if (!ok) {
+      // an abandoned pipeline: wait (bounded) for the loads themselves
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint32_t i = it - 1 - j;
+        mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+        Tile ti;
+        if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
+        const int q = kTall ? ti.rows : ti.cols;
+        const uint32_t idesc = idesc_f8(kRowsP, (q + 15) & ~15);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t st = it % C::kStages, b = it & 1;
+          if (!mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1) ||
+              !mbar_wait(&full[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
+          tc_fence_after();
+          const uint64_t pd = desc0 + (uint64_t)(st * (C::kStageBytes >> 4));
+          const uint64_t qd = pd + (uint64_t)(kPBytes >> 4);
+          const uint32_t d = tmem + b * NT;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f8_ss(d, pd + 2 * k, qd + 2 * k, idesc, k > 0);
+          mma_commit(&empty[st]);
+          mma_commit(&tfull[b]);
+        }
+      }
+      mma_commit(mma_done);                  // nothing may write TMEM once it is freed
+      if (!mbar_wait(mma_done, 0)) fail();
+    }
+    __syncwarp();
+  } else {
+    // ---------------- promotion and store ----------------
+    const int pw = warp - 2, q = warp & 3, part = pw >> 2;   // lane quarter; column part
+    const int c0 = part * C::kCols;
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
+    const int prow = 32 * q + lane;
+    constexpr int kChunk = C::kCols < 32 ? 16 : 32;
+    uint32_t it = 0;
+    bool ok = true;
+    TO* out = static_cast<TO*>(a.out);
+    for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+      Tile ti;
+      if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
+      const int qn = kTall ? ti.rows : ti.cols;            // valid columns of the tile
+      float acc[C::kCols];
+#pragma unroll
+      for (int j = 0; j < C::kCols; ++j) acc[j] = 0.f;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t ss = it % kScaleRing, b = it & 1;
+        if (!mbar_wait(&sfull[ss], (it / kScaleRing) & 1) || !mbar_wait(&tfull[b], (it >> 1) & 1)) {
+          ok = false;
+          fail();
+          break;
+        }
+        tc_fence_after();
+        const float* sc = s_scale + ss * C::kScaleFloats;
+        const float* cs = sc + kRowsP + c0;
+        float rs = sc[kTall ? 0 : prow];
+        if (FORM == WIDE_BLOCK) rs *= sc[kRowsP + c0 / 128];
+#pragma unroll
+        for (int c = 0; c < C::kCols; c += kChunk) {
+          if (c0 + c >= qn) break;                        // uniform in the warp
+          uint32_t r[kChunk];
+          if constexpr (kChunk == 32) pair2::tmem_ld32(tbase + b * NT + c, r);
+          else tmem_ld16(tbase + b * NT + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            const float p = __uint_as_float(r[j]);
+            if constexpr (FORM == WIDE_BLOCK) acc[c + j] = fmaf(p, rs, acc[c + j]);
+            else acc[c + j] = fmaf(p, rs * cs[c + j], acc[c + j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) { mbar_arrive(&tempty[b]); mbar_arrive(&sempty[ss]); }
+      }
+      if (!ok) break;
+      if constexpr (kTall) {
+        if (split > 1) {
+          // this CTA's sums for the cluster: [column][row] over the stages, whose
+          // loads have all been consumed (one tile per CTA when split)
+          float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int j = 0; j < C::kCols; ++j) red[j * kRowsP + prow] = acc[j];
+        } else if (prow < ti.cols) {
+#pragma unroll
+          for (int j = 0; j < C::kCols; ++j)
+            if (j < qn) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, acc[j]);
+        }
+      } else if (prow < ti.rows) {
+        TO* o = out + (size_t)(ti.m0 + prow) * a.ldo + ti.n0 + c0;
+        constexpr int V = 16 / sizeof(TO);
+#pragma unroll
+        for (int j = 0; j < C::kCols; j += V) {
+          if (a.vec && c0 + j + V <= qn) {
+            uint4 v;
+            TO* p = reinterpret_cast<TO*>(&v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) store_val(p + i, acc[j + i]);
+            *reinterpret_cast<uint4*>(o + j) = v;
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (c0 + j + i < qn) store_val(o + j + i, acc[j + i]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (kTall) {
+    if (split > 1) {
+      __syncwarp();
+      pair2::cluster_sync();
+      Tile ti;
+      if (warp >= 2 && first < ntiles && decode<NT, FORM>(a, s_tiles, s_off, first, ti)) {
+        const int prow = 32 * (warp & 3) + lane;
+        const int j0 = NT * (int)rank / split, j1 = min(NT * ((int)rank + 1) / split, ti.rows);
+        TO* out = static_cast<TO*>(a.out);
+        const float* red = reinterpret_cast<const float*>(smem);
+        for (int j = j0; j < j1; ++j) {
+          float v = 0.f;
+          for (int s = 0; s < split; ++s) v += ld_cluster(pair2::map_to_rank(red + j * kRowsP + prow, s));
+          if (prow < ti.cols) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, v);
+        }
+      }
+      __syncwarp();
+      pair2::cluster_sync();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, C::kTmemCols); }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+
+template <int NT, int FORM, typename TO>
+cudaError_t launch_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev,
+                     cudaStream_t st) {
+  using C = Cfg<NT, FORM>;
+  auto kern = fp8_gemm_kernel<NT, FORM, TO>;
+  static bool configured[kMaxDevices] = {};
+  const int smem = C::bytes(g.offsets ? g.n_groups : 0);
+  if (!configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(kMaxGroups));
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  const long brows = (long)(g.offsets ? g.n_groups : 1) * g.N;
+  CUtensorMap am, bm;
+  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, FORM == TALL ? NT : kRowsP) ||
+      !make_tmap_codes(&bm, g.b, brows, g.K, g.ldb, FORM == TALL ? kRowsP : NT))
+    return cudaErrorInvalidValue;
+  Fp8Args a{};
+  a.sa = g.a_scales; a.ldsa = g.lda_scales; a.sb = g.b_scales; a.ldsb = g.ldb_scales;
+  a.offsets = g.offsets; a.out = g.out; a.ldo = g.ldo; a.M = g.M; a.N = g.N;
+  a.KB = ceil_div(g.K, 128); a.G = g.offsets ? g.n_groups : 1; a.NB = ceil_div(g.N, 128);
+  a.split = split;
+  a.vec = (g.ldo * (long)sizeof(TO)) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+  cudaLaunchConfig_t cfg = {};
+  const int resident = sms * (FORM == TALL ? 2 : 1);
+  cfg.gridDim = dim3(split > 1 ? n_tiles * split : (n_tiles < resident ? n_tiles : resident));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, am, bm, a, n_tiles);
+}
+
+template <int NT, int FORM>
+cudaError_t launch_o(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
+  return g.out_dtype == MOE_BF16 ? launch_t<NT, FORM, __nv_bfloat16>(g, n_tiles, split, sms, dev, st)
+                                 : launch_t<NT, FORM, float>(g, n_tiles, split, sms, dev, st);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int G = g.offsets ? g.n_groups : 1, KB = ceil_div(g.K, 128);
+  const bool row_scales = g.ldb_scales > 0;
+  const int mean = (g.M + G - 1) / G;                     // rows per group on average
+  // an upper bound of the tile count: the grouped kernel reads the exact one
+  // from the offsets
+  auto tiles = [&](int rm, int rn) {
+    const long t = ((long)g.M / rm + G) * ceil_div(g.N, rn);
+    const long d = (long)ceil_div(g.M, rm) * ceil_div(g.N, rn);
+    const long n = g.offsets ? t : d;
+    return n > 0x7fffffff ? 0x7fffffff : (int)n;
+  };
+  if (row_scales) return launch_o<256, WIDE_ROW>(g, tiles(128, 256), 1, sms, dev, st);
+  if (mean > 128) return launch_o<256, WIDE_BLOCK>(g, tiles(128, 256), 1, sms, dev, st);
+  const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+  const int n = tiles(nt, 128);
+  int split = 1;
+  if (!g.offsets)
+    while (split < 8 && 2 * split <= KB && (long)n * split * 2 <= 2L * sms) split *= 2;
+  switch (nt) {
+    case 16: return launch_o<16, TALL>(g, n, split, sms, dev, st);
+    case 32: return launch_o<32, TALL>(g, n, split, sms, dev, st);
+    case 64: return launch_o<64, TALL>(g, n, split, sms, dev, st);
+    default: return launch_o<128, TALL>(g, n, split, sms, dev, st);
+  }
+}
+
+cudaError_t fp8_gemm_take_error(int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_fp8_err, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_fp8_err, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace lmoe
