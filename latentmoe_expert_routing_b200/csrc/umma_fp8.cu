@@ -46,8 +46,6 @@ constexpr int kPBytes = kRowsP * kKB;
 constexpr int kScaleRing = 8;
 constexpr int kMaxGroups = 1024;
 
-enum Form { WIDE_BLOCK = 0, WIDE_ROW = 1, TALL = 2 };
-
 struct Fp8Args {
   const float* sa;          // [KB][ldsa]
   long ldsa;
@@ -95,23 +93,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// Arrival on a barrier of either CTA of the pair, for hand-overs of TMEM alone:
+// what it orders are this warp's finished TMEM reads (tcgen05.wait::ld and the
+// fence before it), so no memory has to become visible to the other SM.  The
+// cluster-scope release form costs about 1300 cycles per arrival.
+__device__ __forceinline__ void arrive_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
-template <int NT, int FORM>
-struct Cfg {
-  static constexpr bool kTall = FORM == TALL;
+template <int NT>
+struct TCfg {
   static constexpr int kQBytes = NT * kKB;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kStages = kTall ? (NT <= 32 ? 5 : NT == 64 ? 4 : 3) : 4;
-  static constexpr int kWarps = kTall ? 4 : 16;                 // promoting warps
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int kWarps = 4;                              // promoting warps
   static constexpr int kThreads = 64 + 32 * kWarps;
-  static constexpr int kCols = NT * 4 / kWarps;                 // columns per promoting thread
-  static constexpr int kQScales = FORM == WIDE_BLOCK ? 4 : NT;  // column scales per step
-  static constexpr int kScaleFloats = kRowsP + kQScales;
+  static constexpr int kScaleFloats = 4 + NT;                   // the block's, then the columns'
   static constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
   static constexpr int kScaleOffset = kStages * kStageBytes;
   static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
@@ -129,10 +132,9 @@ struct Tile {
 
 // Tile t: the weight blocks of a group run fastest over its row tiles, so that
 // the CTAs in flight share weight blocks and row tiles through L2.
-template <int NT, int FORM>
+template <int RM, int RN>
 __device__ __forceinline__ bool decode(const Fp8Args& a, const int* s_tiles, const int* s_off, int t,
                                        Tile& o) {
-  constexpr int RM = FORM == TALL ? NT : kRowsP, RN = FORM == TALL ? kRowsP : NT;
   const int nn = (a.N + RN - 1) / RN;
   int lo = 0, base = 0, cnt = a.M;
   if (a.offsets) {
@@ -148,7 +150,7 @@ __device__ __forceinline__ bool decode(const Fp8Args& a, const int* s_tiles, con
   const int nm = (cnt + RM - 1) / RM;
   if (nm <= 0) return false;
   int im, in;
-  if (FORM == TALL) {
+  if (RM < 256) {
     in = t / nm; im = t - in * nm;
   } else {
     // bands of 8 row tiles: a wave's tiles form a block, not a strip
@@ -200,12 +202,11 @@ __device__ void load_groups(const Fp8Args& a, int* s_tiles, int* s_off) {
   }
 }
 
-template <int NT, int FORM, typename TO>
-__global__ void __launch_bounds__(Cfg<NT, FORM>::kThreads, FORM == TALL ? 2 : 1)
-fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+template <int NT, typename TO>
+__global__ void __launch_bounds__(TCfg<NT>::kThreads, 2)
+fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const Fp8Args a, const int n_tiles) {
-  using C = Cfg<NT, FORM>;
-  constexpr bool kTall = FORM == TALL;
+  using C = TCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -223,8 +224,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
   int* s_off = s_tiles + a.G + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kTall && a.split > 1 ? pair2::cluster_rank() : 0u;
-  const int split = kTall ? a.split : 1;
+  const int split = a.split;
+  const uint32_t rank = split > 1 ? pair2::cluster_rank() : 0u;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
@@ -237,7 +238,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     tma_prefetch_desc(&bmap);
   }
   if (warp == 1) { tmem_alloc(tmem_slot, C::kTmemCols); tmem_relinquish(); }
-  load_groups<kTall ? NT : kRowsP, kTall ? kRowsP : NT>(a, s_tiles, s_off);
+  load_groups<NT, kRowsP>(a, s_tiles, s_off);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -257,11 +258,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     bool ok = true;
     for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
       Tile ti;
-      if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
-      const CUtensorMap* pm = kTall ? &bmap : &amap;
-      const CUtensorMap* qm = kTall ? &amap : &bmap;
+      if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
       const int brow = ti.grp * a.N + ti.n0;
-      const int prow = kTall ? brow : ti.m0, qrow = kTall ? ti.m0 : brow;
+      const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t st = it % C::kStages, ss = it % kScaleRing;
         ok = mbar_wait(&empty[st], ((it / C::kStages) & 1) ^ 1) &&
@@ -270,26 +269,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         if (lane == 0) {
           mbar_arrive_expect_tx(&full[st], C::kStageBytes);
           uint8_t* sp = smem + st * C::kStageBytes;
-          tma_load_2d(sp, pm, &full[st], kb * kKB, prow);
-          tma_load_2d(sp + kPBytes, qm, &full[st], kb * kKB, qrow);
+          tma_load_2d(sp, &bmap, &full[st], kb * kKB, brow);
+          tma_load_2d(sp + kPBytes, &amap, &full[st], kb * kKB, ti.m0);
         }
-        // scales: rows first, columns behind them
         float* sc = s_scale + ss * C::kScaleFloats;
         const float* sa = a.sa + (size_t)kb * a.ldsa + ti.m0;
-        if (kTall) {
-          const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB + kb;
-          if (lane == 0) cp_async4(sc, sb, true);
-          for (int i = lane; i < NT; i += 32) cp_async4(sc + kRowsP + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
-        } else {
-          for (int i = lane; i < kRowsP; i += 32) cp_async4(sc + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
-          if (FORM == WIDE_BLOCK) {
-            if (lane < NT / 128 && lane * 128 < ti.cols)
-              cp_async4(sc + kRowsP + lane, a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128 + lane) * a.KB + kb, true);
-          } else {
-            const float* sb = a.sb + (size_t)kb * a.ldsb + ti.n0;
-            for (int i = lane; i < NT; i += 32) cp_async4(sc + kRowsP + i, sb + (i < ti.cols ? i : 0), i < ti.cols);
-          }
-        }
+        if (lane == 0) cp_async4(sc, sb + kb, true);
+        for (int i = lane; i < NT; i += 32) cp_async4(sc + 4 + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
         cp_async_arrive(&sfull[ss]);
       }
     }
@@ -315,9 +301,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       bool ok = true;
       for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
         Tile ti;
-        if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
-        const int q = kTall ? ti.rows : ti.cols;
-        const uint32_t idesc = idesc_f8(kRowsP, (q + 15) & ~15);
+        if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
+        const uint32_t idesc = idesc_f8(kRowsP, (ti.rows + 15) & ~15);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const uint32_t st = it % C::kStages, b = it & 1;
           if (!mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1) ||
@@ -338,21 +323,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     __syncwarp();
   } else {
     // ---------------- promotion and store ----------------
-    const int pw = warp - 2, q = warp & 3, part = pw >> 2;   // lane quarter; column part
-    const int c0 = part * C::kCols;
-    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
-    const int prow = 32 * q + lane;
-    constexpr int kChunk = C::kCols < 32 ? 16 : 32;
+    const int q = warp & 3;                                // TMEM lane quarter
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
+    const int prow = 32 * q + lane;                        // this thread's weight row
+    constexpr int kChunk = NT == 16 || NT == 128 ? 16 : 32;   // 128 sums leave no room for 32
     uint32_t it = 0;
     bool ok = true;
     TO* out = static_cast<TO*>(a.out);
     for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
       Tile ti;
-      if (!decode<NT, FORM>(a, s_tiles, s_off, t, ti)) continue;
-      const int qn = kTall ? ti.rows : ti.cols;            // valid columns of the tile
-      float acc[C::kCols];
+      if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
+      float acc[NT];
 #pragma unroll
-      for (int j = 0; j < C::kCols; ++j) acc[j] = 0.f;
+      for (int j = 0; j < NT; ++j) acc[j] = 0.f;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t ss = it % kScaleRing, b = it & 1;
         if (!mbar_wait(&sfull[ss], (it / kScaleRing) & 1) || !mbar_wait(&tfull[b], (it >> 1) & 1)) {
@@ -362,21 +345,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         }
         tc_fence_after();
         const float* sc = s_scale + ss * C::kScaleFloats;
-        const float* cs = sc + kRowsP + c0;
-        float rs = sc[kTall ? 0 : prow];
-        if (FORM == WIDE_BLOCK) rs *= sc[kRowsP + c0 / 128];
+        const float bs = sc[0];
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += kChunk) {
-          if (c0 + c >= qn) break;                        // uniform in the warp
+        for (int c = 0; c < NT; c += kChunk) {
+          if (c >= ti.rows) break;                         // uniform in the warp
           uint32_t r[kChunk];
           if constexpr (kChunk == 32) pair2::tmem_ld32(tbase + b * NT + c, r);
           else tmem_ld16(tbase + b * NT + c, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const float p = __uint_as_float(r[j]);
-            if constexpr (FORM == WIDE_BLOCK) acc[c + j] = fmaf(p, rs, acc[c + j]);
-            else acc[c + j] = fmaf(p, rs * cs[c + j], acc[c + j]);
+          for (int j = 0; j < kChunk; j += 4) {
+            const float4 cs = *reinterpret_cast<const float4*>(sc + 4 + c + j);
+            acc[c + j] = fmaf(__uint_as_float(r[j]), bs * cs.x, acc[c + j]);
+            acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), bs * cs.y, acc[c + j + 1]);
+            acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), bs * cs.z, acc[c + j + 2]);
+            acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), bs * cs.w, acc[c + j + 3]);
           }
         }
         tc_fence_before();
@@ -384,57 +367,36 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         if (lane == 0) { mbar_arrive(&tempty[b]); mbar_arrive(&sempty[ss]); }
       }
       if (!ok) break;
-      if constexpr (kTall) {
-        if (split > 1) {
-          // this CTA's sums for the cluster: [column][row] over the stages, whose
-          // loads have all been consumed (one tile per CTA when split)
-          float* red = reinterpret_cast<float*>(smem);
+      if (split > 1) {
+        // this CTA's sums for the cluster: [column][row] over the stages, whose
+        // loads have all been consumed (one tile per CTA when split)
+        float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-          for (int j = 0; j < C::kCols; ++j) red[j * kRowsP + prow] = acc[j];
-        } else if (prow < ti.cols) {
+        for (int j = 0; j < NT; ++j) red[j * kRowsP + prow] = acc[j];
+      } else if (prow < ti.cols) {
 #pragma unroll
-          for (int j = 0; j < C::kCols; ++j)
-            if (j < qn) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, acc[j]);
-        }
-      } else if (prow < ti.rows) {
-        TO* o = out + (size_t)(ti.m0 + prow) * a.ldo + ti.n0 + c0;
-        constexpr int V = 16 / sizeof(TO);
-#pragma unroll
-        for (int j = 0; j < C::kCols; j += V) {
-          if (a.vec && c0 + j + V <= qn) {
-            uint4 v;
-            TO* p = reinterpret_cast<TO*>(&v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) store_val(p + i, acc[j + i]);
-            *reinterpret_cast<uint4*>(o + j) = v;
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (c0 + j + i < qn) store_val(o + j + i, acc[j + i]);
-          }
-        }
+        for (int j = 0; j < NT; ++j)
+          if (j < ti.rows) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, acc[j]);
       }
     }
   }
-  if constexpr (kTall) {
-    if (split > 1) {
-      __syncwarp();
-      pair2::cluster_sync();
-      Tile ti;
-      if (warp >= 2 && first < ntiles && decode<NT, FORM>(a, s_tiles, s_off, first, ti)) {
-        const int prow = 32 * (warp & 3) + lane;
-        const int j0 = NT * (int)rank / split, j1 = min(NT * ((int)rank + 1) / split, ti.rows);
-        TO* out = static_cast<TO*>(a.out);
-        const float* red = reinterpret_cast<const float*>(smem);
-        for (int j = j0; j < j1; ++j) {
-          float v = 0.f;
-          for (int s = 0; s < split; ++s) v += ld_cluster(pair2::map_to_rank(red + j * kRowsP + prow, s));
-          if (prow < ti.cols) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, v);
-        }
+  if (split > 1) {
+    __syncwarp();
+    pair2::cluster_sync();
+    Tile ti;
+    if (warp >= 2 && first < ntiles && decode<NT, kRowsP>(a, s_tiles, s_off, first, ti)) {
+      const int prow = 32 * (warp & 3) + lane;
+      const int j0 = NT * (int)rank / split, j1 = min(NT * ((int)rank + 1) / split, ti.rows);
+      TO* out = static_cast<TO*>(a.out);
+      const float* red = reinterpret_cast<const float*>(smem);
+      for (int j = j0; j < j1; ++j) {
+        float v = 0.f;
+        for (int s = 0; s < split; ++s) v += ld_cluster(pair2::map_to_rank(red + j * kRowsP + prow, s));
+        if (prow < ti.cols) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, v);
       }
-      __syncwarp();
-      pair2::cluster_sync();
     }
+    __syncwarp();
+    pair2::cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
@@ -442,38 +404,375 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
+// Wide form: 256 activation rows x 256 weight rows on an SM pair.
+// ---------------------------------------------------------------------------
+constexpr int kWN = 256;                       // weight rows per tile
+constexpr int kWStages = 5;
+constexpr int kWWarps = 8;                     // promoting warps per CTA
+constexpr int kWCols = 128;                    // columns per promoting thread
+constexpr int kWThreads = 128 + 32 * kWWarps;
+// registers: the launch gives 384 x 168 = 64512; the first warpgroup keeps 40 a thread
+// (128 x 40), which leaves the promoting two 232 (256 x 232)
+constexpr int kWRegsLow = 40, kWRegsHigh = 232;
+constexpr int kWStageBytes = 2 * kPBytes;      // 128 activation rows and 128 weight rows
+constexpr int kWOutBytes = 32 * 128;           // output staging of a promoting warp
+
+template <bool ROWS>
+struct WCfg {
+  static constexpr int kScaleFloats = ROWS ? kWN : 0;       // column scales of a step
+  static constexpr int kOutOffset = kWStages * kWStageBytes;
+  static constexpr int kScaleOffset = kOutOffset + kWWarps * kWOutBytes;
+  static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
+  static constexpr int kTableOffset = kBarOffset + 512;
+  static constexpr int bytes(int groups) {
+    return kTableOffset + (groups ? 2 * (groups + 1) * 4 : 0) + 1024;
+  }
+};
+
+// two fp32 fused multiply-adds / products in one instruction
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void mma_pair_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate));
+}
+
+// MMA columns of a pair tile: the valid ones rounded up to 32 (each CTA holds half)
+__device__ __forceinline__ int pair_cols(int cols) { return (cols + 31) & ~31; }
+
+template <bool ROWS, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                const Fp8Args a, const int n_tiles) {
+  using C = WCfg<ROWS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOffset);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);   // the leader's are used
+  uint64_t* done = full + kWStages;                                      // a step's products are
+                                                                         // finished: both CTAs
+  uint64_t* sfull = done + kWStages;                                     // own scales
+  uint64_t* sempty = sfull + kScaleRing;
+  uint64_t* tempty = sempty + kScaleRing;                                // [2] the leader's are used
+  uint64_t* mma_done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_tiles = reinterpret_cast<int*>(smem + C::kTableOffset);
+  int* s_off = s_tiles + a.G + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = pair2::cluster_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWStages; ++s) { mbar_init(&full[s], 1); mbar_init(&done[s], 1); }
+    for (int s = 0; s < kScaleRing; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], kWWarps); }
+    for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * kWWarps);
+    mbar_init(mma_done, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&amap);
+    tma_prefetch_desc(&bmap);
+  }
+  if (warp == 1) { pair2::tmem_alloc_pair(tmem_slot, 512); pair2::tmem_relinquish_pair(); }
+  load_groups<2 * kRowsP, kWN>(a, s_tiles, s_off);
+  tc_fence_before();
+  __syncthreads();
+  pair2::cluster_sync();                 // both CTAs' barriers exist before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int ntiles = a.offsets ? s_tiles[a.G] : n_tiles;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const uint32_t peer_abort = pair2::map_to_rank(const_cast<int*>(abort_flag), rank ^ 1u);
+
+  auto fail = [&]() {
+    atomicOr(&g_fp8_err, DEV_ERR_TIMEOUT);
+    *abort_flag = 1;
+    pair2::store_remote_u32(peer_abort, 1u);
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsLow));
+    if (warp == 0) {
+      // ---------------- tiles by TMA (both CTAs) ----------------
+      if (lane == 0) {
+        const uint32_t full_leader = pair2::map_to_rank(full, 0);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+          Tile ti;
+          if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
+          const int arow = ti.m0 + (int)rank * kRowsP;
+          const int brow = ti.grp * a.N + ti.n0 + (int)rank * (pair_cols(ti.cols) >> 1);
+          for (int kb = 0; kb < a.KB; ++kb, ++it) {
+            const uint32_t st = it % kWStages;
+            if (!mbar_wait(&done[st], ((it / kWStages) & 1) ^ 1)) { ok = false; fail(); break; }
+            uint8_t* sp = smem + st * kWStageBytes;
+            if (leader) mbar_arrive_expect_tx(&full[st], 2 * kWStageBytes);
+            const uint32_t fb = full_leader + st * (uint32_t)sizeof(uint64_t);
+            pair2::tma_load_2d_pair(sp, &amap, fb, kb * kKB, arow);
+            pair2::tma_load_2d_pair(sp + kPBytes, &bmap, fb, kb * kKB, brow);
+          }
+        }
+        // nothing may be in flight into the pair's memory when it ends
+        const uint32_t n = it < (uint32_t)kWStages ? it : (uint32_t)kWStages;
+        for (uint32_t j = 0; j < n && ok; ++j) {
+          const uint32_t i = it - 1 - j;
+          if (!mbar_wait(&done[i % kWStages], (i / kWStages) & 1)) { ok = false; fail(); }
+        }
+        if (!ok && leader)
+          for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t i = it - 1 - j;
+            mbar_wait(&full[i % kWStages], (i / kWStages) & 1);
+          }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- column scales by cp.async (both CTAs) ----------------
+      if constexpr (ROWS) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+          Tile ti;
+          if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
+          const float* sb = a.sb + ti.n0;
+          for (int kb = 0; kb < a.KB; ++kb, ++it, sb += a.ldsb) {
+            const uint32_t ss = it % kScaleRing;
+            ok = mbar_wait(&sempty[ss], ((it / kScaleRing) & 1) ^ 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+            float* sc = s_scale + ss * C::kScaleFloats;
+#pragma unroll
+            for (int i = lane; i < kWN; i += 32) cp_async4(sc + i, sb + (i < ti.cols ? i : 0), i < ti.cols);
+            cp_async_arrive(&sfull[ss]);
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+    } else if (leader && lane == 0) {
+      // ---------------- MMA issuers: warp 1 the even steps, warp 3 the odd ones ----------------
+      // (a step's sum is its own, so the steps need no order among each other)
+      const uint32_t b = warp >> 1;
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      const uint32_t d = tmem + b * kWN;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+        Tile ti;
+        if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
+        const uint32_t idesc = idesc_f8(2 * kRowsP, pair_cols(ti.cols));
+        const uint32_t end = it + a.KB;
+        for (it += (it ^ b) & 1; it < end; it += 2) {
+          const uint32_t st = it % kWStages;
+          if (!mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1) ||
+              !mbar_wait(&full[st], (it / kWStages) & 1)) { ok = false; fail(); break; }
+          tc_fence_after();
+          const uint64_t ad = desc0 + (uint64_t)(st * (kWStageBytes >> 4));
+          const uint64_t bd = ad + (uint64_t)(kPBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_pair_f8(d, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+          pair2::commit_pair_both(&done[st]);
+        }
+        it = end;
+      }
+      pair2::commit_pair_local(mma_done);
+      if (!mbar_wait(mma_done, 0)) fail();
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsHigh));
+    // ---------------- promotion and store (both CTAs) ----------------
+    const int q = warp & 3, half = (warp - 4) >> 2, c0 = half * kWCols;
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
+    const uint32_t tempty_leader = pair2::map_to_rank(tempty, 0);
+    const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
+    uint8_t* stage = smem + C::kOutOffset + (warp - 4) * kWOutBytes;
+    TO* out = static_cast<TO*>(a.out);
+    uint32_t it = 0;
+    // scales of this thread's row (times its 128 columns' block scale) are read
+    // three steps ahead; those of the next tile's first steps before this tile
+    // is written out
+    const float *pa = nullptr, *pb = nullptr;
+    float sa[3], sb[3];
+    auto open = [&](const Tile& ti) {
+      const int row = r0 + lane;
+      pa = a.sa + ti.m0 + (row < ti.rows ? row : 0);
+      pb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128 + (c0 < ti.cols ? half : 0)) * a.KB;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        sa[i] = i < a.KB ? __ldg(pa + (size_t)i * a.ldsa) : 0.f;
+        sb[i] = !ROWS && i < a.KB ? __ldg(pb + i) : 1.f;
+      }
+      pa += 3 * a.ldsa;
+      pb += 3;
+    };
+    Tile ti;
+    int t = first;
+    bool ok = t < ntiles && decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti);
+    if (ok) open(ti);
+    while (ok && !*abort_flag) {
+      const int qn = ti.cols;
+      uint64_t acc[kWCols / 2];
+#pragma unroll
+      for (int j = 0; j < kWCols / 2; ++j) acc[j] = 0;
+      for (int kb = 0; kb < a.KB; ++kb, ++it) {
+        const uint32_t ss = it % kScaleRing, b = it & 1;
+        const float rs = sa[0] * sb[0];
+        sa[0] = sa[1]; sa[1] = sa[2]; sb[0] = sb[1]; sb[1] = sb[2];
+        if (kb + 3 < a.KB) {
+          sa[2] = __ldg(pa);
+          pa += a.ldsa;
+          if (!ROWS) sb[2] = __ldg(pb++);
+        }
+        if ((ROWS && !mbar_wait(&sfull[ss], (it / kScaleRing) & 1)) ||
+            !mbar_wait(&done[it % kWStages], (it / kWStages) & 1)) {
+          ok = false;
+          fail();
+          break;
+        }
+        tc_fence_after();
+        const uint64_t rs2 = pack2(__float_as_uint(rs), __float_as_uint(rs));
+        const float* cs = s_scale + ss * C::kScaleFloats + c0;
+#pragma unroll
+        for (int c = 0; c < kWCols; c += 64) {
+          if (c0 + c >= qn) break;                         // uniform in the warp
+          uint32_t r[2][32];
+          pair2::tmem_ld32(tbase + b * kWN + c, r[0]);
+          pair2::tmem_ld32(tbase + b * kWN + c + 32, r[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 64; j += 4) {
+            const uint32_t* p = &r[j >> 5][j & 31];
+            uint64_t* s = &acc[(c + j) >> 1];
+            if constexpr (ROWS) {
+              const uint4 w = *reinterpret_cast<const uint4*>(cs + c + j);
+              s[0] = fma2(pack2(p[0], p[1]), mul2(rs2, pack2(w.x, w.y)), s[0]);
+              s[1] = fma2(pack2(p[2], p[3]), mul2(rs2, pack2(w.z, w.w)), s[1]);
+            } else {
+              s[0] = fma2(pack2(p[0], p[1]), rs2, s[0]);
+              s[1] = fma2(pack2(p[2], p[3]), rs2, s[1]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          arrive_tmem(tempty_leader + b * (uint32_t)sizeof(uint64_t));
+          if (ROWS) mbar_arrive(&sempty[ss]);
+        }
+      }
+      if (!ok) break;
+      const Tile cur = ti;
+      t += step;
+      ok = t < ntiles && decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti);
+      if (ok) open(ti);
+      // out: 128 bytes of each of the warp's 32 rows at a time through shared
+      // memory (16-byte pieces, exclusive-or swizzled), so that a store
+      // instruction writes whole 128-byte runs of four rows
+      constexpr int V = 16 / sizeof(TO), W = 8 * V;        // columns per piece, per pass
+      const int rows = cur.rows - r0;
+#pragma unroll
+      for (int c = 0; c < kWCols; c += W) {
+        if (c0 + c >= qn) break;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          uint4 v;
+          TO* e = reinterpret_cast<TO*>(&v);
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            float lo, hi;
+            unpack2(acc[(c + h * V + i) >> 1], lo, hi);
+            store_val(e + i, lo);
+            store_val(e + i + 1, hi);
+          }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
+        }
+        __syncwarp();
+        const int h = lane & 7, col = c0 + c + h * V;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((h ^ (r & 7)) << 4));
+          if (r < rows) {
+            TO* o = out + (size_t)(cur.m0 + r0 + r) * a.ldo + cur.n0 + col;
+            if (a.vec && col + V <= qn) {
+              *reinterpret_cast<uint4*>(o) = v;
+            } else {
+              const TO* e = reinterpret_cast<const TO*>(&v);
+#pragma unroll
+              for (int x = 0; x < V; ++x)
+                if (col + x < qn) o[x] = e[x];
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  pair2::cluster_sync();                 // the leader's MMAs and both CTAs' loads are done
+  if (warp == 1) { tc_fence_after(); pair2::tmem_dealloc_pair(tmem, 512); }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 constexpr int kMaxDevices = 64;
 
-template <int NT, int FORM, typename TO>
-cudaError_t launch_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev,
-                     cudaStream_t st) {
-  using C = Cfg<NT, FORM>;
-  auto kern = fp8_gemm_kernel<NT, FORM, TO>;
-  static bool configured[kMaxDevices] = {};
-  const int smem = C::bytes(g.offsets ? g.n_groups : 0);
-  if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(kMaxGroups));
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  const long brows = (long)(g.offsets ? g.n_groups : 1) * g.N;
-  CUtensorMap am, bm;
-  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, FORM == TALL ? NT : kRowsP) ||
-      !make_tmap_codes(&bm, g.b, brows, g.K, g.ldb, FORM == TALL ? kRowsP : NT))
-    return cudaErrorInvalidValue;
+Fp8Args args_of(const moe_fp8_gemm& g) {
+  const long es = g.out_dtype == MOE_BF16 ? 2 : 4;
   Fp8Args a{};
   a.sa = g.a_scales; a.ldsa = g.lda_scales; a.sb = g.b_scales; a.ldsb = g.ldb_scales;
   a.offsets = g.offsets; a.out = g.out; a.ldo = g.ldo; a.M = g.M; a.N = g.N;
   a.KB = ceil_div(g.K, 128); a.G = g.offsets ? g.n_groups : 1; a.NB = ceil_div(g.N, 128);
+  a.split = 1;
+  a.vec = (g.ldo * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+  return a;
+}
+
+template <int NT, typename TO>
+cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
+  using C = TCfg<NT>;
+  auto kern = fp8_tall_kernel<NT, TO>;
+  static bool configured[kMaxDevices] = {};
+  if (!configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::bytes(kMaxGroups));
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  Fp8Args a = args_of(g);
   a.split = split;
-  a.vec = (g.ldo * (long)sizeof(TO)) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+  CUtensorMap am, bm;
+  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, NT) ||
+      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const int resident = sms * (FORM == TALL ? 2 : 1);
-  cfg.gridDim = dim3(split > 1 ? n_tiles * split : (n_tiles < resident ? n_tiles : resident));
+  cfg.gridDim = dim3(split > 1 ? n_tiles * split : (n_tiles < 2 * sms ? n_tiles : 2 * sms));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = C::bytes(g.offsets ? g.n_groups : 0);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -484,10 +783,43 @@ cudaError_t launch_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int
   return cudaLaunchKernelEx(&cfg, kern, am, bm, a, n_tiles);
 }
 
-template <int NT, int FORM>
-cudaError_t launch_o(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
-  return g.out_dtype == MOE_BF16 ? launch_t<NT, FORM, __nv_bfloat16>(g, n_tiles, split, sms, dev, st)
-                                 : launch_t<NT, FORM, float>(g, n_tiles, split, sms, dev, st);
+template <int NT>
+cudaError_t tall(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
+  return g.out_dtype == MOE_BF16 ? tall_t<NT, __nv_bfloat16>(g, n_tiles, split, sms, dev, st)
+                                 : tall_t<NT, float>(g, n_tiles, split, sms, dev, st);
+}
+
+template <bool ROWS, typename TO>
+cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStream_t st) {
+  using C = WCfg<ROWS>;
+  auto kern = fp8_pair_kernel<ROWS, TO>;
+  static int pairs[kMaxDevices] = {};            // co-resident pairs (0: not asked yet)
+  if (!pairs[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::bytes(kMaxGroups));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sms / 2));
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = C::bytes(kMaxGroups);
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+    pairs[dev] = n > 0 ? n : 1;
+  }
+  const Fp8Args a = args_of(g);
+  CUtensorMap am, bm;
+  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, kRowsP) ||
+      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP))
+    return cudaErrorInvalidValue;
+  const int n = n_tiles < pairs[dev] ? n_tiles : pairs[dev];
+  kern<<<2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st>>>(am, bm, a, n_tiles);
+  return cudaGetLastError();
+}
+
+template <bool ROWS>
+cudaError_t wide(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStream_t st) {
+  return g.out_dtype == MOE_BF16 ? wide_t<ROWS, __nv_bfloat16>(g, n_tiles, sms, dev, st)
+                                 : wide_t<ROWS, float>(g, n_tiles, sms, dev, st);
 }
 
 }  // namespace
@@ -499,28 +831,27 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int G = g.offsets ? g.n_groups : 1, KB = ceil_div(g.K, 128);
-  const bool row_scales = g.ldb_scales > 0;
   const int mean = (g.M + G - 1) / G;                     // rows per group on average
-  // an upper bound of the tile count: the grouped kernel reads the exact one
-  // from the offsets
+  // an upper bound of the tile count: a grouped kernel reads the exact one from
+  // the offsets
   auto tiles = [&](int rm, int rn) {
     const long t = ((long)g.M / rm + G) * ceil_div(g.N, rn);
     const long d = (long)ceil_div(g.M, rm) * ceil_div(g.N, rn);
     const long n = g.offsets ? t : d;
     return n > 0x7fffffff ? 0x7fffffff : (int)n;
   };
-  if (row_scales) return launch_o<256, WIDE_ROW>(g, tiles(128, 256), 1, sms, dev, st);
-  if (mean > 128) return launch_o<256, WIDE_BLOCK>(g, tiles(128, 256), 1, sms, dev, st);
+  if (g.ldb_scales > 0) return wide<true>(g, tiles(256, 256), sms, dev, st);
+  if (mean > 128) return wide<false>(g, tiles(256, 256), sms, dev, st);
   const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
   const int n = tiles(nt, 128);
   int split = 1;
   if (!g.offsets)
     while (split < 8 && 2 * split <= KB && (long)n * split * 2 <= 2L * sms) split *= 2;
   switch (nt) {
-    case 16: return launch_o<16, TALL>(g, n, split, sms, dev, st);
-    case 32: return launch_o<32, TALL>(g, n, split, sms, dev, st);
-    case 64: return launch_o<64, TALL>(g, n, split, sms, dev, st);
-    default: return launch_o<128, TALL>(g, n, split, sms, dev, st);
+    case 16: return tall<16>(g, n, split, sms, dev, st);
+    case 32: return tall<32>(g, n, split, sms, dev, st);
+    case 64: return tall<64>(g, n, split, sms, dev, st);
+    default: return tall<128>(g, n, split, sms, dev, st);
   }
 }
 
