@@ -703,8 +703,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           for (int i = 0; i < V; i += 2) {
             float lo, hi;
             unpack2(acc[(c + h * V + i) >> 1], lo, hi);
-            store_val(e + i, lo);
-            store_val(e + i + 1, hi);
+            if constexpr (sizeof(TO) == 2) *reinterpret_cast<__nv_bfloat162*>(e + i) = __floats2bfloat162_rn(lo, hi);
+            else { e[i] = lo; e[i + 1] = hi; }
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
         }
