@@ -24,7 +24,8 @@ namespace {
 
 __device__ int g_group_err;            // DEV_ERR_INDEX: an expert index out of range
 
-constexpr int kRows = 8;               // rows (warps) per CTA
+constexpr int kRows = 8;               // rows (warps) per CTA, at most
+constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -36,60 +37,42 @@ __device__ __forceinline__ float sigmoid_score(float l) {
   return __double2float_rn(__ddiv_rn(1.0, __dadd_rn(1.0, exp_fixed(a))));
 }
 
-// exp(l - m) for l <= m: below -700 the quotient rounds to 0 in fp32; l == m
-// covers rows whose maximum is +inf.
+// exp(l - m) in fp64 for l <= m: a = n ln 2 + r, |r| <= ln 2 / 2, and the Taylor
+// polynomial of degree 13 (truncated below 2^-57).  Below -700 the quotient by
+// the sum rounds to 0 in fp32; l == m covers rows whose maximum is +inf.
 __device__ __forceinline__ double softmax_term(float l, float m) {
   if (l == m) return 1.0;
-  return exp_fixed(fmax((double)l - (double)m, -700.0));
+  const double a = fmax((double)l - (double)m, -700.0);
+  const double n = rint(a * 0x1.71547652b82fep+0);
+  const double r = fma(n, -0x1.a39ef35793c76p-33, fma(n, -0x1.62e42fee00000p-1, a));
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return p * __longlong_as_double((long long)((int)n + 1023) << 52);
 }
 
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.f);        // -0 orders as +0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
 
 // Keys order as choice scores do; experts out of the selection and experts
 // already taken come below every score.
 constexpr uint32_t kKeyOut = 1u, kKeyTaken = 0u;
-
-// Group step for one row held by a warp (lane: experts lane + 32 i).
-template <int EPL>
-__device__ void drop_groups(float (&c)[EPL], int E, int n_group, int topk_group, int lane, float* gs) {
-  const int G = E / n_group;
-  for (int g = 0; g < n_group; ++g) {
-    float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= g * G && e < (g + 1) * G) { m1 = fmaxf(m1, fminf(m0, c[i])); m0 = fmaxf(m0, c[i]); }
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-      const float o0 = __shfl_xor_sync(0xffffffffu, m0, off), o1 = __shfl_xor_sync(0xffffffffu, m1, off);
-      m1 = fmaxf(fminf(m0, o0), fmaxf(m1, o1));
-      m0 = fmaxf(m0, o0);
-    }
-    if (lane == 0) gs[g] = __fadd_rn(m0, m1);
-  }
-  __syncwarp();
-  uint64_t keep = 0;
-  for (int g0 = 0; g0 < n_group; g0 += 32) {
-    const int g = g0 + lane;
-    bool kg = false;
-    if (g < n_group) {
-      int r = 0;
-      for (int o = 0; o < n_group; ++o) r += (gs[o] > gs[g] || (gs[o] == gs[g] && o < g)) ? 1 : 0;
-      kg = r < topk_group;
-    }
-    keep |= (uint64_t)__ballot_sync(0xffffffffu, kg) << g0;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E && !((keep >> (e / G)) & 1ull)) c[i] = -INFINITY;
-  }
-  __syncwarp();
-}
 
 struct TopkArgs {
   const void* logits;
@@ -102,37 +85,88 @@ struct TopkArgs {
   float* w;
 };
 
+// The two largest of each group of G consecutive experts, added: lane g returns
+// the sums of groups g and g + 32.  c goes through shared memory, a group's
+// stretch starting G | 1 floats behind the last one's (an odd stride, so lanes
+// reading their own groups meet no bank conflicts).
+template <int EPL>
+__device__ __forceinline__ void group_sums(const float (&c)[EPL], int E, int n_group, int lane,
+                                           float* buf, float (&sum)[2]) {
+  const int G = E / n_group, st = G | 1;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) buf[e / G * st + e % G] = c[i];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float m0 = -INFINITY, m1 = -INFINITY;
+    if (lane + 32 * h < n_group)
+      for (int j = 0; j < G; ++j) {
+        const float v = buf[(lane + 32 * h) * st + j];
+        m1 = fmaxf(m1, fminf(m0, v));
+        m0 = fmaxf(m0, v);
+      }
+    sum[h] = __fadd_rn(m0, m1);
+  }
+  __syncwarp();
+}
+
+// bit mask of the topk_group best groups (ties: lower group)
+__device__ __forceinline__ uint64_t best_groups(const float (&sum)[2], int n_group, int topk_group, int lane) {
+  int r0 = 0, r1 = 0;
+  for (int o = 0; o < n_group; ++o) {
+    const float v = __shfl_sync(kAll, o < 32 ? sum[0] : sum[1], o & 31);
+    r0 += v > sum[0] || (v == sum[0] && o < lane);
+    r1 += v > sum[1] || (v == sum[1] && o < lane + 32);
+  }
+  const unsigned k0 = __ballot_sync(kAll, lane < n_group && r0 < topk_group);
+  const unsigned k1 = __ballot_sync(kAll, lane + 32 < n_group && r1 < topk_group);
+  return (uint64_t)k1 << 32 | k0;
+}
+
+// The weights of one row from its scores in slot order.
+__device__ __forceinline__ void write_weights(const TopkArgs& a, long t, const float* sel, int lane) {
+  float den = 1.f;
+  if (a.renorm) {
+    float S = 0.f;
+    for (int j = 0; j < a.k; ++j) S = __fadd_rn(S, sel[j]);
+    den = __fadd_rn(S, 1e-20f);
+  }
+  for (int j = lane; j < a.k; j += 32) {
+    const float v = a.renorm ? __fdiv_rn(sel[j], den) : sel[j];
+    a.w[(size_t)t * a.k + j] = __fmul_rn(v, a.scale);
+  }
+}
+
+// One row, every score evaluated exactly and k rounds of a warp arg-max: rows
+// that the quick way cannot decide (more than 32 experts next to the border,
+// fewer eligible experts than slots, k > 32, groups whose order the bounds
+// leave open).
 template <typename TL, int EPL, bool SOFTMAX>
-__global__ void __launch_bounds__(32 * kRows)
-route_topk_kernel(const TopkArgs a) {
-  __shared__ float s_sel[kRows][64];
-  __shared__ float s_grp[kRows][64];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kRows + warp;
-  if (t >= a.T) return;
+__device__ __noinline__ void select_exact(const TopkArgs& a, long t, int lane, float* sel, float* buf) {
   const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.ld;
   float s[EPL], c[EPL];
+  uint32_t live = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 32 * i;
     s[i] = e < a.E ? load_logit(row + e) : -INFINITY;
-    if (!(s[i] > -INFINITY)) s[i] = -INFINITY;             // NaN counts as -inf
+    live |= (s[i] > -INFINITY ? 1u : 0u) << i;               // NaN is out as well
   }
-  uint32_t live = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) live |= (s[i] > -INFINITY ? 1u : 0u) << i;
   if (SOFTMAX) {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) m = fmaxf(m, s[i]);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (live >> i & 1u) sum += softmax_term(s[i], m);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       s[i] = live >> i & 1u ? __double2float_rn(__ddiv_rn(softmax_term(s[i], m), sum)) : 0.f;
@@ -142,44 +176,247 @@ route_topk_kernel(const TopkArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
     c[i] = -INFINITY;
-    if (live >> i & 1u) c[i] = a.bias ? __fadd_rn(s[i], a.bias[e]) : s[i];
-    if (!(c[i] > -INFINITY)) c[i] = -INFINITY;             // a NaN bias takes its expert out
+    if (live >> i & 1u) c[i] = a.bias ? __fadd_rn(s[i], a.bias[lane + 32 * i]) : s[i];
+    if (!(c[i] > -INFINITY)) c[i] = -INFINITY;               // a NaN bias takes its expert out
   }
-  if (a.n_group > 1) drop_groups<EPL>(c, a.E, a.n_group, a.topk_group, lane, s_grp[warp]);
+  if (a.n_group > 1) {
+    float gs[2];
+    group_sums<EPL>(c, a.E, a.n_group, lane, buf, gs);
+    const uint64_t keep = best_groups(gs, a.n_group, a.topk_group, lane);
+    const int G = a.E / a.n_group;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 32 * i;
+      if (e < a.E && !(keep >> (e / G) & 1)) c[i] = -INFINITY;
+    }
+  }
   uint32_t key[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e >= a.E ? kKeyTaken : c[i] > -INFINITY ? order_key(c[i]) : kKeyOut;
-  }
+  for (int i = 0; i < EPL; ++i)
+    key[i] = lane + 32 * i >= a.E ? kKeyTaken : c[i] > -INFINITY ? order_key(c[i]) : kKeyOut;
   for (int j = 0; j < a.k; ++j) {
     uint32_t best = 0;
     int bi = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (key[i] > best) { best = key[i]; bi = i; }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)(lane + 32 * bi) : 0xffffffffu);
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    const int e = (int)__reduce_min_sync(kAll, best == top ? (unsigned)(lane + 32 * bi) : kAll);
     if ((e & 31) == lane) {
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         if (i == e >> 5) { v = top > kKeyOut ? s[i] : 0.f; key[i] = kKeyTaken; }
-      s_sel[warp][j] = v;
+      sel[j] = v;
       a.idx[(size_t)t * a.k + j] = e;
     }
   }
   __syncwarp();
-  float den = 1.f;
-  if (a.renorm) {
-    float S = 0.f;
-    for (int j = 0; j < a.k; ++j) S = __fadd_rn(S, s_sel[warp][j]);
-    den = __fadd_rn(S, 1e-20f);
+  write_weights(a, t, sel, lane);
+}
+
+// A row per warp.  Sorting exact scores is not needed to find the top k: fp32
+// scores with an error bound d leave only the experts next to the border open.
+//   1. c~ = s~ + b with |c~ - c| <= d: lo = c~ - d, hi = c~ + d
+//   2. tau with at least k experts of lo >= tau, by bisection over the ordered
+//      floats between the smallest lane maximum (32 experts reach it) and the
+//      largest; an expert of hi < tau is beaten by k others for sure
+//   3. the others, at most 32, one per lane: exact score in fp64, rank by
+//      counting (score descending, expert ascending), slot = rank
+// so a row costs one fp64 score per lane and not E / 32.  The bound: the argument
+// of ex2.approx, |l| log2 e in fp32, is off by half a unit and by the constant's
+// rounding, together 1.2e-6 of the exponential at |l| = 16 and 4.9e-6 at 80;
+// ex2.approx, the sum and the quotient add 4.1e-7, so that s~ is within 2^-19 of
+// s up to 16 and 2^-17 up to 80.  Below -80 the argument stays there: s and s~
+// are under 2e-35, which kappa * 1e-29 covers.  Softmax has its exponentials from
+// fp64, for the sum: four fp32 roundings, 2^-21.  The roundings of c~, s and c are
+// 2^-24 of |c| and s each.
+template <typename TL, int EPL, bool SOFTMAX>
+__global__ void __launch_bounds__(32 * kRows)
+route_topk_kernel(const TopkArgs a) {
+  extern __shared__ float s_dyn[];
+  __shared__ float s_sel[kRows][64];
+  __shared__ uint64_t s_key[kRows][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = blockDim.x >> 5;
+  float* buf = s_dyn + (size_t)warp * (a.E + 64);          // n_group > 1 only
+  float* sel = s_sel[warp];
+  uint64_t* keys = s_key[warp];
+  float b[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
+
+  for (long t = (long)blockIdx.x * warps + warp; t < a.T; t += (long)gridDim.x * warps) {
+    const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.ld;
+    float lo[EPL], hi[EPL];
+    float m = -INFINITY, big = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) lo[i] = lane + 32 * i < a.E ? load_logit(row + lane + 32 * i) : -INFINITY;
+    double sum = 1.0;
+    float kappa;
+    if (SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) m = fmaxf(m, lo[i]);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const double e = lo[i] > -INFINITY ? softmax_term(lo[i], m) : 0.0;
+        hi[i] = lo[i] > -INFINITY ? (float)e : -INFINITY;
+        sum += e;
+      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+      const float inv = 1.f / (float)sum;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) lo[i] = hi[i] > -INFINITY ? hi[i] * inv : -INFINITY;
+      kappa = 0x1p-21f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float l = lo[i];
+        if (l > -INFINITY) big = fmaxf(big, fabsf(l));
+        lo[i] = l > -INFINITY ? __fdividef(1.f, 1.f + __expf(-fmaxf(l, -80.f))) : -INFINITY;
+      }
+      kappa = __any_sync(kAll, big > 16.f) ? 0x1p-17f : 0x1p-19f;
+    }
+    // lo holds s~, -inf for experts that are out
+    bool open = false;
+    if (a.n_group > 1) {
+      float c[EPL], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        c[i] = lo[i] > -INFINITY ? lo[i] + b[i] : -INFINITY;
+        if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
+        else top = fmaxf(top, fabsf(c[i]) + lo[i]);
+      }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+      float gs[2];
+      group_sums<EPL>(c, a.E, a.n_group, lane, buf, gs);
+      const uint64_t keep = best_groups(gs, a.n_group, a.topk_group, lane);
+      // the worst kept and the best dropped group have to differ by more than
+      // twice the error of a sum of two scores
+      float kept = INFINITY, dropped = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < a.n_group) {
+          if (keep >> (lane + 32 * h) & 1) kept = fminf(kept, gs[h]);
+          else dropped = fmaxf(dropped, gs[h]);
+        }
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) {
+        kept = fminf(kept, __shfl_xor_sync(kAll, kept, off));
+        dropped = fmaxf(dropped, __shfl_xor_sync(kAll, dropped, off));
+      }
+      open |= a.topk_group < a.n_group && !(kept - dropped > 8.f * kappa * (top + 1e-29f));
+      const int G = a.E / a.n_group;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e < a.E && !(keep >> (e / G) & 1)) lo[i] = -INFINITY;
+      }
+    }
+    uint32_t mine = 0;                                     // largest key of this lane
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float c = lo[i] + b[i];
+      if (lo[i] > -INFINITY && c > -INFINITY) {
+        const float d = kappa * (lo[i] + fabsf(c) + 1e-29f);
+        open |= !(d < INFINITY);                           // an infinite bias
+        lo[i] = c - d;
+        hi[i] = c + d;
+        mine = max(mine, order_key(lo[i]));
+        ++n;
+      } else {
+        lo[i] = hi[i] = -INFINITY;
+      }
+    }
+    n = __reduce_add_sync(kAll, n);                        // eligible experts
+    open = __any_sync(kAll, open) || n < a.k || a.k > 32;
+    if (!open && n > 32) {
+      uint32_t L = __reduce_min_sync(kAll, mine), H = __reduce_max_sync(kAll, mine) + 1u;
+      // a lane without an expert: start below every score
+      if (L == 0u) L = order_key(-INFINITY) + 1u;
+      float tau = key_float(L);
+      while (true) {
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) n += hi[i] >= tau;
+        n = __reduce_add_sync(kAll, n);
+        if (n <= 32) break;
+        // raise tau: the middle, or halfway down from it while fewer than k reach it
+        bool moved = false;
+        while (H - L > 1u) {
+          const uint32_t mid = L + ((H - L) >> 1);
+          const float x = key_float(mid);
+          int r = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) r += lo[i] >= x;
+          r = __reduce_add_sync(kAll, r);
+          if (r >= a.k) { L = mid; tau = x; moved = true; break; }
+          H = mid;
+        }
+        if (!moved) { open = true; break; }
+      }
+      if (!open) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) mask |= (hi[i] >= tau ? 1u : 0u) << i;
+        int at = __popc(mask), total = at;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int v = __shfl_up_sync(kAll, at, off);
+          if (lane >= off) at += v;
+        }
+        at -= total;
+        for (; mask; mask &= mask - 1) keys[at++] = (uint64_t)(lane + 32 * (__ffs(mask) - 1));
+      }
+    } else if (!open) {
+      // at most 32 eligible experts: all of them
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) mask |= (hi[i] > -INFINITY ? 1u : 0u) << i;
+      int at = __popc(mask), total = at;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kAll, at, off);
+        if (lane >= off) at += v;
+      }
+      at -= total;
+      for (; mask; mask &= mask - 1) keys[at++] = (uint64_t)(lane + 32 * (__ffs(mask) - 1));
+    }
+    if (open) {
+      select_exact<TL, EPL, SOFTMAX>(a, t, lane, sel, buf);
+      __syncwarp();
+      continue;
+    }
+    __syncwarp();
+    const int e = lane < n ? (int)keys[lane] : 0;
+    float s = 0.f;
+    uint64_t key = 0;
+    if (lane < n) {
+      const float l = load_logit(row + e);
+      s = SOFTMAX ? __double2float_rn(__ddiv_rn(softmax_term(l, m), sum)) : sigmoid_score(l);
+      const float c = a.bias ? __fadd_rn(s, a.bias[e]) : s;
+      key = (uint64_t)order_key(c) << 32 | (uint32_t)(0xffff - e);
+    }
+    __syncwarp();
+    keys[lane] = key;
+    __syncwarp();
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += keys[j] > key;
+    if (lane < n && rank < a.k) {
+      sel[rank] = s;
+      a.idx[(size_t)t * a.k + rank] = e;
+    }
+    __syncwarp();
+    write_weights(a, t, sel, lane);
+    __syncwarp();
   }
-  for (int j = lane; j < a.k; j += 32)
-    a.w[(size_t)t * a.k + j] = __fmul_rn(__fdiv_rn(s_sel[warp][j], den), a.scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -291,12 +528,16 @@ route_topk_bwd_kernel(const TopkBwdArgs a) {
 
 template <typename TL, bool SOFTMAX>
 cudaError_t topk_launch(const TopkArgs& a, cudaStream_t st) {
-  const int grid = ceil_div(a.T, kRows), epl = ceil_div(a.E, 32);
-  if (epl <= 1) route_topk_kernel<TL, 1, SOFTMAX><<<grid, 32 * kRows, 0, st>>>(a);
-  else if (epl <= 4) route_topk_kernel<TL, 4, SOFTMAX><<<grid, 32 * kRows, 0, st>>>(a);
-  else if (epl <= 8) route_topk_kernel<TL, 8, SOFTMAX><<<grid, 32 * kRows, 0, st>>>(a);
-  else if (epl <= 16) route_topk_kernel<TL, 16, SOFTMAX><<<grid, 32 * kRows, 0, st>>>(a);
-  else route_topk_kernel<TL, 32, SOFTMAX><<<grid, 32 * kRows, 0, st>>>(a);
+  // few rows: one warp per CTA, so that each has an SM's issue slots to itself
+  const int warps = a.T >= 2048 ? kRows : a.T >= 512 ? 4 : 1;
+  const int need = ceil_div(a.T, warps), grid = need < 148 * 8 ? need : 148 * 8;
+  const int threads = 32 * warps, epl = ceil_div(a.E, 32);
+  const size_t sm = a.n_group > 1 ? (size_t)warps * (a.E + 64) * 4 : 0;      // at most 34 KB
+  if (epl <= 1) route_topk_kernel<TL, 1, SOFTMAX><<<grid, threads, sm, st>>>(a);
+  else if (epl <= 4) route_topk_kernel<TL, 4, SOFTMAX><<<grid, threads, sm, st>>>(a);
+  else if (epl <= 8) route_topk_kernel<TL, 8, SOFTMAX><<<grid, threads, sm, st>>>(a);
+  else if (epl <= 16) route_topk_kernel<TL, 16, SOFTMAX><<<grid, threads, sm, st>>>(a);
+  else route_topk_kernel<TL, 32, SOFTMAX><<<grid, threads, sm, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -314,8 +555,8 @@ cudaError_t topk_bwd_launch(const TopkBwdArgs& a, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Grouping: a stable counting sort of the pairs p = t k + j by expert.  Blocks
-// of kPairs consecutive pairs count their experts, one block scans the counts
-// of every (expert, block), and the blocks place their pairs.  A pair's rank
+// of kPairs consecutive pairs count their experts, a warp per expert scans its
+// counts over the blocks, and the blocks place their pairs.  A pair's rank
 // among its block's pairs of the same expert is the number of such pairs in
 // earlier warps (a column of s_cnt) plus those in lower lanes (match mask), so
 // the order never depends on the order in which atomics arrive.  Pairs with an
@@ -348,28 +589,31 @@ group_count_kernel(const GroupArgs a) {
   for (int e = threadIdx.x; e < a.E; e += kPairs) a.blk[(size_t)e * a.nblk + blockIdx.x] = s_hist[e];
 }
 
-__global__ void __launch_bounds__(1024)
+// a warp per expert: its counts over the blocks become exclusive prefixes
+__global__ void __launch_bounds__(256)
 group_scan_kernel(const GroupArgs a) {
-  __shared__ int s_tot[1024], s_warp[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = warp; e < a.E; e += 32) {
-    int run = 0;
-    for (int b0 = 0; b0 < a.nblk; b0 += 32) {
-      const int b = b0 + lane;
-      const int v = b < a.nblk ? a.blk[(size_t)e * a.nblk + b] : 0;
-      int x = v;
+  const int lane = threadIdx.x & 31, e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (e >= a.E) return;
+  int32_t* c = a.blk + (size_t)e * a.nblk;
+  int run = 0;
+  for (int b0 = 0; b0 < a.nblk; b0 += 32) {
+    const int b = b0 + lane;
+    const int v = b < a.nblk ? c[b] : 0;
+    int x = v;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-      }
-      if (b < a.nblk) a.blk[(size_t)e * a.nblk + b] = run + x - v;
-      run += __shfl_sync(0xffffffffu, x, 31);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
-    if (lane == 0) s_tot[e] = run;
+    if (b < a.nblk) c[b] = run + x - v;
+    run += __shfl_sync(0xffffffffu, x, 31);
   }
-  __syncthreads();
-  const int e = threadIdx.x, v = e < a.E ? s_tot[e] : 0;
+  if (lane == 0) a.counts[e] = run;
+}
+
+// exclusive prefix of v over the block's 1024 threads
+__device__ __forceinline__ int block_prefix(int v, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -378,18 +622,29 @@ group_scan_kernel(const GroupArgs a) {
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  int before = 0;
-  for (int i = 0; i < warp; ++i) before += s_warp[i];
-  if (e < a.E) { a.counts[e] = v; a.offsets[e + 1] = before + x; }
-  if (e == 0) a.offsets[0] = 0;
+  int before = lane < warp ? s_warp[lane] : 0;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+  return before + x - v;
 }
 
+// places a block's pairs; every block adds up the experts' counts for itself,
+// the first writes them out as offsets
 __global__ void __launch_bounds__(kPairs)
 group_place_kernel(const GroupArgs a) {
   extern __shared__ uint8_t s_cnt[];                   // [32 warps][E] pairs of a warp
+  __shared__ int s_base[1024], s_warp[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < 8 * a.E; i += kPairs) reinterpret_cast<uint32_t*>(s_cnt)[i] = 0u;
-  __syncthreads();
+  const int c = threadIdx.x < a.E ? a.counts[threadIdx.x] : 0;
+  const int off = block_prefix(c, s_warp);             // (a barrier: s_cnt is cleared)
+  if (threadIdx.x < a.E) {
+    s_base[threadIdx.x] = off + a.blk[(size_t)threadIdx.x * a.nblk + blockIdx.x];
+    if (blockIdx.x == 0) {
+      a.offsets[threadIdx.x] = off;
+      if (threadIdx.x == a.E - 1) a.offsets[a.E] = off + c;
+    }
+  }
   const long p = (long)blockIdx.x * kPairs + threadIdx.x;
   int e = p < a.P ? a.idx[p] : -1;
   if (e >= a.E) e = -1;
@@ -399,7 +654,7 @@ group_place_kernel(const GroupArgs a) {
   __syncthreads();
   if (p >= a.P) return;
   if (e < 0) { a.pos[p] = -1; return; }
-  int q = a.offsets[e] + a.blk[(size_t)e * a.nblk + blockIdx.x] + below;
+  int q = s_base[e] + below;
   for (int i = 0; i < warp; ++i) q += s_cnt[i * a.E + e];
   a.pos[p] = q;
   a.perm[q] = (int32_t)p;
@@ -438,7 +693,7 @@ cudaError_t launch_route_group(const int32_t* idx, long P, int E, int32_t* count
   const GroupArgs a{idx, P, E, ceil_div(P, kPairs), counts, offsets, perm, pos,
                     static_cast<int32_t*>(ws)};
   group_count_kernel<<<a.nblk, kPairs, (size_t)E * 4, st>>>(a);
-  group_scan_kernel<<<1, 1024, 0, st>>>(a);
+  group_scan_kernel<<<ceil_div(E, 8), 256, 0, st>>>(a);
   group_place_kernel<<<a.nblk, kPairs, (size_t)E * 32, st>>>(a);
   return cudaGetLastError();
 }
