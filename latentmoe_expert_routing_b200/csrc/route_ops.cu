@@ -14,6 +14,8 @@
 //
 // Why fp64 scores: selection compares neighbouring values, and an fp32 sigmoid
 // or softmax is off by several units in the last place, enough to swap them.
+#include <float.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "router_math.cuh"
@@ -66,13 +68,15 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t b = __float_as_uint(f + 0.f);        // -0 orders as +0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float key_float(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-
 // Keys order as choice scores do; experts out of the selection and experts
 // already taken come below every score.
 constexpr uint32_t kKeyOut = 1u, kKeyTaken = 0u;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+  return v;
+}
 
 struct TopkArgs {
   const void* logits;
@@ -126,17 +130,21 @@ __device__ __forceinline__ uint64_t best_groups(const float (&sum)[2], int n_gro
   return (uint64_t)k1 << 32 | k0;
 }
 
-// The weights of one row from its scores in slot order.
+// The weights of one row from its scores in slot order; sel is zero from slot k
+// to the next multiple of 4.
 __device__ __forceinline__ void write_weights(const TopkArgs& a, long t, const float* sel, int lane) {
   float den = 1.f;
   if (a.renorm) {
     float S = 0.f;
-    for (int j = 0; j < a.k; ++j) S = __fadd_rn(S, sel[j]);
+    for (int j = 0; j < a.k; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(sel + j);
+      S = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(S, v.x), v.y), v.z), v.w);
+    }
     den = __fadd_rn(S, 1e-20f);
   }
   for (int j = lane; j < a.k; j += 32) {
     const float v = a.renorm ? __fdiv_rn(sel[j], den) : sel[j];
-    a.w[(size_t)t * a.k + j] = __fmul_rn(v, a.scale);
+    a.w[t * a.k + j] = __fmul_rn(v, a.scale);
   }
 }
 
@@ -209,96 +217,115 @@ __device__ __noinline__ void select_exact(const TopkArgs& a, long t, int lane, f
       for (int i = 0; i < EPL; ++i)
         if (i == e >> 5) { v = top > kKeyOut ? s[i] : 0.f; key[i] = kKeyTaken; }
       sel[j] = v;
-      a.idx[(size_t)t * a.k + j] = e;
+      a.idx[t * a.k + j] = e;
     }
   }
+  if (lane < 3 && a.k + lane < 64) sel[a.k + lane] = 0.f;
   __syncwarp();
   write_weights(a, t, sel, lane);
 }
 
-// A row per warp.  Sorting exact scores is not needed to find the top k: fp32
-// scores with an error bound d leave only the experts next to the border open.
-//   1. c~ = s~ + b with |c~ - c| <= d: lo = c~ - d, hi = c~ + d
-//   2. tau with at least k experts of lo >= tau, by bisection over the ordered
-//      floats between the smallest lane maximum (32 experts reach it) and the
-//      largest; an expert of hi < tau is beaten by k others for sure
-//   3. the others, at most 32, one per lane: exact score in fp64, rank by
-//      counting (score descending, expert ascending), slot = rank
-// so a row costs one fp64 score per lane and not E / 32.  The bound: the argument
-// of ex2.approx, |l| log2 e in fp32, is off by half a unit and by the constant's
-// rounding, together 1.2e-6 of the exponential at |l| = 16 and 4.9e-6 at 80;
-// ex2.approx, the sum and the quotient add 4.1e-7, so that s~ is within 2^-19 of
-// s up to 16 and 2^-17 up to 80.  Below -80 the argument stays there: s and s~
-// are under 2e-35, which kappa * 1e-29 covers.  Softmax has its exponentials from
-// fp64, for the sum: four fp32 roundings, 2^-21.  The roundings of c~, s and c are
-// 2^-24 of |c| and s each.
+// A row per warp.  Exact scores of all experts are not needed to find the top k:
+// an order value c~ per expert, within d of a value that orders as the choice
+// scores do, leaves only the experts next to the border open.
+//   1. c~ = s~ + b from fp32 arithmetic; for softmax without a bias the logit
+//      itself (the score rises with it)
+//   2. tau that at least k experts reach (c~ >= tau), by bisection between the
+//      smallest lane maximum, which 32 experts reach, and the largest value.  An
+//      expert of c~ < tau - 2 d is beaten by k others
+//   3. the rest, at most 32, one per lane: exact score in fp64, rank by counting
+//      (score descending, expert ascending), slot = rank
+// so a row costs one fp64 score per lane and not E / 32.
+//
+// Bounds.  Sigmoid: the argument of ex2.approx, |l| log2 e in fp32, is off by
+// half a unit and by the constant's rounding, together 1.2e-6 of the exponential
+// at |l| = 16 and 4.9e-6 at 80; ex2.approx, the sum and the quotient add 4.1e-7:
+// s~ is within kappa s, kappa = 2^-19 up to 16 and 2^-17 up to 80.  Below -80 the
+// argument stays there: s and s~ are under 2e-35.  Softmax has its exponentials
+// from fp64, for the sum: four fp32 roundings, kappa = 2^-21.  The roundings of
+// c~, s and c are 2^-24 of |c| and s each, so d = kappa (2 max s + max |b|) + 1e-34
+// covers every expert.  Logits as order values: scores whose logits differ by
+// 2^-20 differ by 2^-20 of themselves and round to different fp32 numbers while
+// they are normal, which holds for l - m > -80 (a sum of at most 1024).
+//
+// A row takes about 1000 warp instructions at 512 experts, and instruction issue
+// is what bounds it: 16384 x 512, k = 22, ROUTE_US us, against 92 us for fp64
+// scores of all experts and k arg-max rounds.
 template <typename TL, int EPL, bool SOFTMAX>
-__global__ void __launch_bounds__(32 * kRows)
+__global__ void __launch_bounds__(32 * kRows, EPL <= 8 ? 5 : EPL == 16 ? 4 : 2)
 route_topk_kernel(const TopkArgs a) {
   extern __shared__ float s_dyn[];
-  __shared__ float s_sel[kRows][64];
-  __shared__ uint64_t s_key[kRows][32];
+  __shared__ __align__(16) float s_sel[kRows][64];
+  __shared__ __align__(16) uint64_t s_key[kRows][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5;
   float* buf = s_dyn + (size_t)warp * (a.E + 64);          // n_group > 1 only
   float* sel = s_sel[warp];
   uint64_t* keys = s_key[warp];
-  float b[EPL];
+  float b[EPL], bmax = 0.f;
+  const bool by_logit = SOFTMAX && !a.bias && a.n_group == 1;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
+  for (int i = 0; i < EPL; ++i) {
+    b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
+    if (b[i] > -INFINITY) bmax = fmaxf(bmax, fabsf(b[i]));   // an expert out by its bias has no say
+  }
+  bmax = warp_max(bmax);
 
   for (long t = (long)blockIdx.x * warps + warp; t < a.T; t += (long)gridDim.x * warps) {
     const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.ld;
-    float lo[EPL], hi[EPL];
-    float m = -INFINITY, big = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) lo[i] = lane + 32 * i < a.E ? load_logit(row + lane + 32 * i) : -INFINITY;
+    float c[EPL];                                          // -inf: not eligible
+    float m = -INFINITY, d;
     double sum = 1.0;
-    float kappa;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = lane + 32 * i < a.E ? load_logit(row + lane + 32 * i) : -INFINITY;
     if (SOFTMAX) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) m = fmaxf(m, lo[i]);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+      for (int i = 0; i < EPL; ++i) m = fmaxf(m, c[i]);
+      m = warp_max(m);
       sum = 0.0;
+      if (by_logit) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const double e = lo[i] > -INFINITY ? softmax_term(lo[i], m) : 0.0;
-        hi[i] = lo[i] > -INFINITY ? (float)e : -INFINITY;
-        sum += e;
+        for (int i = 0; i < EPL; ++i) {
+          if (c[i] > -INFINITY) sum += softmax_term(c[i], m);
+          else c[i] = -INFINITY;                           // NaN
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+        d = 0x1p-21f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const double e = c[i] > -INFINITY ? softmax_term(c[i], m) : 0.0;
+          c[i] = c[i] > -INFINITY ? (float)e : -INFINITY;
+          sum += e;
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+        const float inv = 1.f / (float)sum;                // the largest score as well
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = fmaf(c[i], inv, b[i]);
+        d = 0x1p-21f * (2.f * inv + bmax) + 1e-34f;
       }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      const float inv = 1.f / (float)sum;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) lo[i] = hi[i] > -INFINITY ? hi[i] * inv : -INFINITY;
-      kappa = 0x1p-21f;
     } else {
+      float big = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const float l = lo[i];
-        if (l > -INFINITY) big = fmaxf(big, fabsf(l));
-        lo[i] = l > -INFINITY ? __fdividef(1.f, 1.f + __expf(-fmaxf(l, -80.f))) : -INFINITY;
+        const float l = c[i], x = fmaxf(l, -80.f);
+        big = fmaxf(big, fabsf(x));
+        c[i] = l > -INFINITY ? __fdividef(1.f, 1.f + __expf(-x)) + b[i] : -INFINITY;
       }
-      kappa = __any_sync(kAll, big > 16.f) ? 0x1p-17f : 0x1p-19f;
+      d = (__any_sync(kAll, big > 16.f) ? 0x1p-17f : 0x1p-19f) * (2.f + bmax) + 1e-34f;
     }
-    // lo holds s~, -inf for experts that are out
-    bool open = false;
+    bool open = !(d < INFINITY) || a.k > 32;               // an infinite bias
     if (a.n_group > 1) {
-      float c[EPL], top = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        c[i] = lo[i] > -INFINITY ? lo[i] + b[i] : -INFINITY;
-        if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
-        else top = fmaxf(top, fabsf(c[i]) + lo[i]);
-      }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+      for (int i = 0; i < EPL; ++i)
+        if (!(c[i] > -INFINITY)) c[i] = -INFINITY;         // a NaN bias
       float gs[2];
       group_sums<EPL>(c, a.E, a.n_group, lane, buf, gs);
       const uint64_t keep = best_groups(gs, a.n_group, a.topk_group, lane);
       // the worst kept and the best dropped group have to differ by more than
-      // twice the error of a sum of two scores
+      // twice the error of a sum of two scores, whose rounding d covers too
       float kept = INFINITY, dropped = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -306,113 +333,106 @@ route_topk_kernel(const TopkArgs a) {
           if (keep >> (lane + 32 * h) & 1) kept = fminf(kept, gs[h]);
           else dropped = fmaxf(dropped, gs[h]);
         }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) {
-        kept = fminf(kept, __shfl_xor_sync(kAll, kept, off));
-        dropped = fmaxf(dropped, __shfl_xor_sync(kAll, dropped, off));
-      }
-      open |= a.topk_group < a.n_group && !(kept - dropped > 8.f * kappa * (top + 1e-29f));
+      kept = -warp_max(-kept);
+      dropped = warp_max(dropped);
+      open |= a.topk_group < a.n_group && !(kept - dropped > 8.f * d);
       const int G = a.E / a.n_group;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = lane + 32 * i;
-        if (e < a.E && !(keep >> (e / G) & 1)) lo[i] = -INFINITY;
+        if (e < a.E && !(keep >> (e / G) & 1)) c[i] = -INFINITY;
       }
     }
-    uint32_t mine = 0;                                     // largest key of this lane
-    int n = 0;
+    float top = -INFINITY, low = INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float c = lo[i] + b[i];
-      if (lo[i] > -INFINITY && c > -INFINITY) {
-        const float d = kappa * (lo[i] + fabsf(c) + 1e-29f);
-        open |= !(d < INFINITY);                           // an infinite bias
-        lo[i] = c - d;
-        hi[i] = c + d;
-        mine = max(mine, order_key(lo[i]));
-        ++n;
-      } else {
-        lo[i] = hi[i] = -INFINITY;
-      }
+      if (!SOFTMAX || !by_logit) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;   // a NaN bias
+      top = fmaxf(top, c[i]);
+      if (lane + 32 * i < a.E) low = fminf(low, c[i]);
     }
-    n = __reduce_add_sync(kAll, n);                        // eligible experts
-    open = __any_sync(kAll, open) || n < a.k || a.k > 32;
+    int n = a.E;                                           // eligible experts
+    if (!__all_sync(kAll, low > -INFINITY)) {
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) n += c[i] > -INFINITY;
+      n = __reduce_add_sync(kAll, n);
+    }
+    open |= n < a.k;
+    float cut = -FLT_MAX;                                  // candidates: c >= cut
     if (!open && n > 32) {
-      uint32_t L = __reduce_min_sync(kAll, mine), H = __reduce_max_sync(kAll, mine) + 1u;
-      // a lane without an expert: start below every score
-      if (L == 0u) L = order_key(-INFINITY) + 1u;
-      float tau = key_float(L);
+      // a lane without an expert: start at the lowest finite value
+      float lo = fmaxf(-warp_max(-top), -FLT_MAX), hi = warp_max(top);
       while (true) {
+        cut = lo - 2.f * d;
         n = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) n += hi[i] >= tau;
+        for (int i = 0; i < EPL; ++i) n += c[i] >= cut;
         n = __reduce_add_sync(kAll, n);
-        if (n <= 32) break;
-        // raise tau: the middle, or halfway down from it while fewer than k reach it
+        if (n <= 32) {
+          open = by_logit && lo - m < -80.f;
+          break;
+        }
+        // raise lo: to the middle, or down towards it while fewer than k reach that
         bool moved = false;
-        while (H - L > 1u) {
-          const uint32_t mid = L + ((H - L) >> 1);
-          const float x = key_float(mid);
+        while (true) {
+          const float x = 0.5f * lo + 0.5f * hi;
+          if (!(x > lo && x < hi)) break;
           int r = 0;
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) r += lo[i] >= x;
+          for (int i = 0; i < EPL; ++i) r += c[i] >= x;
           r = __reduce_add_sync(kAll, r);
-          if (r >= a.k) { L = mid; tau = x; moved = true; break; }
-          H = mid;
+          if (r < a.k) { hi = x; continue; }
+          lo = x;
+          moved = true;
+          if (r <= 32) break;
         }
         if (!moved) { open = true; break; }
       }
-      if (!open) {
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) mask |= (hi[i] >= tau ? 1u : 0u) << i;
-        int at = __popc(mask), total = at;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int v = __shfl_up_sync(kAll, at, off);
-          if (lane >= off) at += v;
-        }
-        at -= total;
-        for (; mask; mask &= mask - 1) keys[at++] = (uint64_t)(lane + 32 * (__ffs(mask) - 1));
-      }
-    } else if (!open) {
-      // at most 32 eligible experts: all of them
-      uint32_t mask = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) mask |= (hi[i] > -INFINITY ? 1u : 0u) << i;
-      int at = __popc(mask), total = at;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(kAll, at, off);
-        if (lane >= off) at += v;
-      }
-      at -= total;
-      for (; mask; mask &= mask - 1) keys[at++] = (uint64_t)(lane + 32 * (__ffs(mask) - 1));
+    } else if (by_logit) {
+      open |= __any_sync(kAll, low > -INFINITY && low - m < -80.f);
     }
     if (open) {
       select_exact<TL, EPL, SOFTMAX>(a, t, lane, sel, buf);
       __syncwarp();
       continue;
     }
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) mask |= (c[i] >= cut ? 1u : 0u) << i;
+    const int own = __popc(mask);
+    int at = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kAll, at, off);
+      if (lane >= off) at += v;
+    }
+    at -= own;
+    int* cand = reinterpret_cast<int*>(sel);
+    for (; mask; mask &= mask - 1) cand[at++] = lane + 32 * (__ffs(mask) - 1);
     __syncwarp();
-    const int e = lane < n ? (int)keys[lane] : 0;
+    const int e = cand[lane < n ? lane : 0];
     float s = 0.f;
     uint64_t key = 0;
     if (lane < n) {
       const float l = load_logit(row + e);
       s = SOFTMAX ? __double2float_rn(__ddiv_rn(softmax_term(l, m), sum)) : sigmoid_score(l);
-      const float c = a.bias ? __fadd_rn(s, a.bias[e]) : s;
-      key = (uint64_t)order_key(c) << 32 | (uint32_t)(0xffff - e);
+      const float v = a.bias ? __fadd_rn(s, a.bias[e]) : s;
+      key = (uint64_t)order_key(v) << 32 | (uint32_t)(0xffff - e);
     }
-    __syncwarp();
-    keys[lane] = key;
+    keys[lane] = key;                                      // 0, below all, past n
     __syncwarp();
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > key;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(keys + j);
+      rank += v.x > key;
+      rank += v.y > key;
+    }
     if (lane < n && rank < a.k) {
       sel[rank] = s;
-      a.idx[(size_t)t * a.k + rank] = e;
+      a.idx[t * a.k + rank] = e;
     }
+    if (lane < 3 && a.k + lane < 64) sel[a.k + lane] = 0.f;
     __syncwarp();
     write_weights(a, t, sel, lane);
     __syncwarp();
