@@ -21,11 +21,6 @@ import torch
 
 from . import binding as B
 
-_F32, _BF16, _I32, _F8 = torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn
-_CODE = {_F32: B.MOE_FP32, _BF16: B.MOE_BF16}
-_OUT = {"fp32": _F32, "bf16": _BF16}
-
-
 class Fp8(NamedTuple):
     """E4M3 codes and their fp32 scales, one for each block of 128.
 
@@ -54,54 +49,67 @@ class NormBackward(NamedTuple):
     dgate: Optional[torch.Tensor]
 
 
+# The calls are short next to a decoding step, so what surrounds them is kept
+# short too: the current stream's raw handle, sizes as numbers (torch.empty takes
+# them faster than a tuple), checks in line.
+_device = torch._C._cuda_getDevice
+_set_device = torch.cuda.set_device
+_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+_F32, _BF16, _I32, _F8, _U8 = (torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn,
+                               torch.uint8)
+_CODE = {_F32: B.MOE_FP32, _BF16: B.MOE_BF16}
+_OUT = {"fp32": _F32, "bf16": _BF16}
+
+
 class _on:
-    """Makes the tensors' device current for a call; `_on(dev).stream` is its
-    current stream."""
+    """Makes a device current for a call; entered only when it is not."""
 
     def __init__(self, dev):
-        self.dev, self.old = dev.index, torch.cuda.current_device()
+        self.dev = dev
 
     def __enter__(self):
-        if self.dev != self.old:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
+        self.old = _device()
+        _set_device(self.dev)
 
     def __exit__(self, *exc):
-        if self.dev != self.old:
-            torch.cuda.set_device(self.old)
+        _set_device(self.old)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _bad(what):
+    raise ValueError(what)
 
 
-def _dtype(t, what):
-    _need(t.dtype in _CODE, f"{what} must be float32 or bfloat16")
-    return _CODE[t.dtype]
+def _input(t, what, dims=2):
+    """The device index and dtype code of a cuda fp32 / bf16 matrix."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _bad(f"{what} must be a cuda tensor")
+    if t.dim() != dims:
+        _bad(f"{what} must have {dims} dimensions")
+    dt = _CODE.get(t.dtype)
+    if dt is None:
+        _bad(f"{what} must be float32 or bfloat16")
+    return t.get_device(), dt
 
 
-def _same(dev, **tensors):
-    for n, t in tensors.items():
-        _need(t is None or t.device == dev, f"{n} must be on {dev}")
-
-
-def _cuda(t, what):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{what} must be a cuda tensor")
-    return t.device
+def _like(t, what, dev, dtype, shape):
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _bad(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
 
 
 def _rows(t):
     """t [R, C] with contiguous rows, and their stride; a copy where t's are not."""
-    if t.stride(1) != 1 and t.shape[1] != 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
-        t = t.contiguous()
-    return t, max(t.stride(0), t.shape[1])
+    R, C = t.shape
+    sr, sc = t.stride()
+    if sc != 1 and C != 1 or sr < C and R > 1:
+        return t.contiguous(), C
+    return t, sr if sr > C else C
 
 
 def _rows16(t):
     """The same, each row starting on 16 bytes."""
     t, ld = _rows(t)
-    if t.data_ptr() % 16 or ld * t.element_size() % 16:
+    if t.data_ptr() & 15 or ld * t.element_size() & 15:
         t = t.clone(memory_format=torch.contiguous_format)
         ld = t.shape[1]
     return t, ld
@@ -109,7 +117,7 @@ def _rows16(t):
 
 def _vec16(t):
     t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def _up16(n):
@@ -120,10 +128,6 @@ def _blocks(n):
     return (n + 127) // 128
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 # ---------------------------------------------------------------------------
 # routing
 # ---------------------------------------------------------------------------
@@ -132,63 +136,75 @@ def route_topk(logits, k, *, bias=None, score="sigmoid", n_group=1, topk_group=1
     """Top-k experts and their weights for given router logits [T, E] (fp32 or
     bf16): (idx [T, k] int32, w [T, k] fp32).  bias [E] fp32 enters the selection
     only; -inf logits take experts out of a row (moe_route_topk)."""
-    dev = _cuda(logits, "logits")
-    _need(logits.dim() == 2, "logits must be [T, E]")
-    dt = _dtype(logits, "logits")
-    _need(score in B.SCORE, f"score must be one of {sorted(B.SCORE)}")
+    dev, dt = _input(logits, "logits")
+    if score not in B.SCORE:
+        _bad(f"score must be one of {sorted(B.SCORE)}")
+    if dev != _device():
+        with _on(dev):
+            return route_topk(logits, k, bias=bias, score=score, n_group=n_group,
+                              topk_group=topk_group, renorm=renorm, scale=scale)
     T, E = logits.shape
     if bias is not None:
-        _same(dev, bias=bias)
-        _need(bias.dtype == _F32 and bias.shape == (E,), "bias must be an fp32 [E] tensor")
+        _like(bias, "bias", dev, _F32, (E,))
         bias = bias.contiguous()
-    with _on(dev) as st:
-        logits, ld = _rows(logits)
-        idx = torch.empty((T, k), dtype=_I32, device=dev)
-        w = torch.empty((T, k), dtype=_F32, device=dev)
-        B.moe_route_topk(_ptr(logits), dt, ld, _ptr(bias), T, E, k, B.SCORE[score], n_group,
-                         topk_group, int(renorm), scale, _ptr(idx), _ptr(w), st)
+    logits, ld = _rows(logits)
+    idx = _empty(T, k, dtype=_I32, device=logits.device)
+    w = _empty(T, k, dtype=_F32, device=logits.device)
+    B.moe_route_topk(logits.data_ptr(), dt, ld, None if bias is None else bias.data_ptr(), T, E, k,
+                     B.SCORE[score], n_group, topk_group, 1 if renorm else 0, scale,
+                     idx.data_ptr(), w.data_ptr(), _stream(dev))
     return idx, w
 
 
 def route_topk_backward(logits, idx, w, dw, *, score="sigmoid", renorm=True, scale=1.0):
     """Gradient of the logits from dw [T, k], given route_topk's arguments and
     results: dlogits [T, E] in the logits' type."""
-    dev = _cuda(logits, "logits")
-    _need(logits.dim() == 2 and idx.dim() == 2, "logits must be [T, E] and idx [T, k]")
-    dt = _dtype(logits, "logits")
-    _need(score in B.SCORE, f"score must be one of {sorted(B.SCORE)}")
+    dev, dt = _input(logits, "logits")
+    if score not in B.SCORE:
+        _bad(f"score must be one of {sorted(B.SCORE)}")
+    if dev != _device():
+        with _on(dev):
+            return route_topk_backward(logits, idx, w, dw, score=score, renorm=renorm, scale=scale)
     T, E = logits.shape
+    if idx.dim() != 2:
+        _bad("idx must be [T, k]")
     k = idx.shape[1]
-    _same(dev, idx=idx, w=w, dw=dw)
-    _need(idx.dtype == _I32 and idx.shape[0] == T, "idx must be int32 [T, k]")
-    _need(w.dtype == _F32 and w.shape == idx.shape, "w must be fp32 [T, k]")
-    _need(dw.dtype == _F32 and dw.shape == idx.shape, "dw must be fp32 [T, k]")
-    with _on(dev) as st:
-        logits, ld = _rows(logits)
-        idx, w, dw = idx.contiguous(), w.contiguous(), dw.contiguous()
-        dl = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        B.moe_route_topk_backward(_ptr(logits), dt, ld, _ptr(idx), _ptr(w), _ptr(dw), T, E, k,
-                                  B.SCORE[score], int(renorm), scale, _ptr(dl), E, st)
+    _like(idx, "idx", dev, _I32, (T, k))
+    _like(w, "w", dev, _F32, (T, k))
+    _like(dw, "dw", dev, _F32, (T, k))
+    logits, ld = _rows(logits)
+    idx, w, dw = idx.contiguous(), w.contiguous(), dw.contiguous()
+    dl = _empty(T, E, dtype=logits.dtype, device=logits.device)
+    B.moe_route_topk_backward(logits.data_ptr(), dt, ld, idx.data_ptr(), w.data_ptr(),
+                              dw.data_ptr(), T, E, k, B.SCORE[score], 1 if renorm else 0, scale,
+                              dl.data_ptr(), E, _stream(dev))
     return dl
 
 
 def route_group(idx, n_experts):
     """The pairs t*k + j of idx [T, k] by expert: (counts [E], offsets [E + 1],
-    perm [T*k], pos [T*k]), int32 (moe_route_group)."""
-    dev = _cuda(idx, "idx")
-    _need(idx.dim() == 2 and idx.dtype == _I32, "idx must be int32 [T, k]")
+    perm [T*k], pos [T*k]), int32, views of one buffer (moe_route_group)."""
+    if not (isinstance(idx, torch.Tensor) and idx.is_cuda):
+        _bad("idx must be a cuda tensor")
+    if idx.dim() != 2 or idx.dtype != _I32:
+        _bad("idx must be int32 [T, k]")
+    dev = idx.get_device()
+    if dev != _device():
+        with _on(dev):
+            return route_group(idx, n_experts)
     T, k = idx.shape
-    with _on(dev) as st:
-        idx = idx.contiguous()
-        counts = torch.empty(n_experts, dtype=_I32, device=dev)
-        offsets = torch.empty(n_experts + 1, dtype=_I32, device=dev)
-        perm = torch.empty(T * k, dtype=_I32, device=dev)
-        pos = torch.empty(T * k, dtype=_I32, device=dev)
-        n = B.moe_route_group_workspace(T, k, n_experts)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        B.moe_route_group(_ptr(idx), T, k, n_experts, _ptr(counts), _ptr(offsets), _ptr(perm),
-                          _ptr(pos), _ptr(ws), n, st)
-    return counts, offsets, perm, pos
+    idx = idx.contiguous()
+    E, P = n_experts, T * k
+    need = B.moe_route_group_workspace(T, k, E)
+    ws = (need + 15) // 16 * 4                    # the workspace lies in front
+    buf = _empty(max(0, ws + 2 * E + 1 + 2 * P), dtype=_I32, device=idx.device)
+    at = buf.data_ptr()
+    counts = at + 4 * ws
+    B.moe_route_group(idx.data_ptr(), T, k, E, counts, counts + 4 * E, counts + 4 * (2 * E + 1),
+                      counts + 4 * (2 * E + 1 + P), at, need, _stream(dev))
+    v = buf.as_strided
+    return (v((E,), (1,), ws), v((E + 1,), (1,), ws + E), v((P,), (1,), ws + 2 * E + 1),
+            v((P,), (1,), ws + 2 * E + 1 + P))
 
 
 # ---------------------------------------------------------------------------
@@ -197,37 +213,35 @@ def route_group(idx, n_experts):
 def _gate_kind(gate, T, D):
     if gate is None:
         return B.MOE_GATE_NONE
-    if gate.dim() == 1 and gate.shape[0] == D:
+    if gate.shape == (D,):
         return B.MOE_GATE_CHANNEL
-    _need(gate.dim() == 2 and gate.shape[0] == T and gate.shape[1] in (1, D),
-          "gate must be [D], [T, 1] or [T, D]")
-    return B.MOE_GATE_FULL if gate.shape[1] == D and D > 1 else B.MOE_GATE_TOKEN
+    if gate.shape == (T, D) and D > 1:
+        return B.MOE_GATE_FULL
+    if gate.shape != (T, 1):
+        _bad("gate must be [D], [T, 1] or [T, D]")
+    return B.MOE_GATE_TOKEN
 
 
-def _norm_args(shape, dtype, dev, y, r, post_weight, gate, residual_scale, pre_weight, eps):
-    """The fields that forward and backward share; the tensors that its
-    pointers come from are kept in the second result."""
-    T, D = shape
-    a = B.moe_norm_args(T=T, D=D, dtype=_CODE[dtype], residual_scale=residual_scale, eps=eps)
-    a.gate_kind = _gate_kind(gate, T, D)
-    for n, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        _need(w is None or (w.dtype == dtype and w.shape == (D,)), f"{n} must be [D] in x's type")
-    _need(gate is None or gate.dtype == dtype, "gate must have x's type")
-    _same(dev, y=y, post_weight=post_weight, pre_weight=pre_weight, gate=gate)
-    _need(y.shape == shape and y.dtype == dtype, "y must have x's shape and type")
+def _norm_args(T, D, dt, x, y, r, post_weight, gate, residual_scale, pre_weight, eps):
+    """The fields that forward and backward share; the tensors whose pointers
+    they hold are kept in the second result."""
+    a = B.moe_norm_args(T, D, dt, _gate_kind(gate, T, D), residual_scale, eps)
+    dev, dtype = r.get_device(), r.dtype
+    if y.shape != r.shape or y.dtype != dtype or y.get_device() != dev:
+        _bad("y must have x's shape, type and device")
     y, a.ldy = _rows16(y)
-    keep = [y]
     a.y = y.data_ptr()
-    if r is not None:
-        r, a.ldr = _rows16(r)
-        a.r = r.data_ptr()
-        keep.append(r)
-    for n, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if w is not None:
-            w = _vec16(w)
-            setattr(a, n, w.data_ptr())
-            keep.append(w)
+    if post_weight is not None:
+        _like(post_weight, "post_weight", dev, dtype, (D,))
+        post_weight = _vec16(post_weight)
+        a.post_weight = post_weight.data_ptr()
+    if pre_weight is not None:
+        _like(pre_weight, "pre_weight", dev, dtype, (D,))
+        pre_weight = _vec16(pre_weight)
+        a.pre_weight = pre_weight.data_ptr()
     if gate is not None:
+        if gate.dtype != dtype or gate.get_device() != dev:
+            _bad("gate must have x's type and device")
         if a.gate_kind == B.MOE_GATE_FULL:
             gate, a.ldg = _rows16(gate)
         elif a.gate_kind == B.MOE_GATE_TOKEN:
@@ -236,8 +250,7 @@ def _norm_args(shape, dtype, dev, y, r, post_weight, gate, residual_scale, pre_w
         else:
             gate = _vec16(gate)
         a.gate = gate.data_ptr()
-        keep.append(gate)
-    return a, keep
+    return a, (y, post_weight, pre_weight, gate)
 
 
 def norm_residual(x, y, *, post_weight=None, gate=None, residual_scale=1.0, pre_weight=None,
@@ -246,28 +259,31 @@ def norm_residual(x, y, *, post_weight=None, gate=None, residual_scale=1.0, pre_
     h = norm(r; pre_weight), x and y [T, D] fp32 or bf16.  gate: None, [D],
     [T, 1] or [T, D].  stats keeps the reciprocal norms, which
     norm_residual_backward reads."""
-    dev = _cuda(x, "x")
-    _need(x.dim() == 2, "x must be [T, D]")
-    _dtype(x, "x")
+    dev, dt = _input(x, "x")
+    if dev != _device():
+        with _on(dev):
+            return norm_residual(x, y, post_weight=post_weight, gate=gate,
+                                 residual_scale=residual_scale, pre_weight=pre_weight, eps=eps,
+                                 stats=stats)
     T, D = x.shape
-    with _on(dev) as st:
-        a, keep = _norm_args(x.shape, x.dtype, dev, y, None, post_weight, gate, residual_scale,
-                             pre_weight, eps)
-        x, a.ldx = _rows16(x)
-        a.x = x.data_ptr()
-        r = torch.empty((T, D), dtype=x.dtype, device=dev)
-        a.r, a.ldr = r.data_ptr(), D
-        h = ry = rr = None
-        if pre_weight is not None:
-            h = torch.empty((T, D), dtype=x.dtype, device=dev)
-            a.h, a.ldh = h.data_ptr(), D
-        if stats and post_weight is not None:
-            ry = torch.empty(T, dtype=_F32, device=dev)
+    where, dtype = x.device, x.dtype
+    a, keep = _norm_args(T, D, dt, x, y, x, post_weight, gate, residual_scale, pre_weight, eps)
+    x, a.ldx = _rows16(x)
+    a.x = x.data_ptr()
+    r = _empty(T, D, dtype=dtype, device=where)
+    a.r, a.ldr = r.data_ptr(), D
+    h = ry = rr = None
+    if pre_weight is not None:
+        h = _empty(T, D, dtype=dtype, device=where)
+        a.h, a.ldh = h.data_ptr(), D
+    if stats:
+        if post_weight is not None:
+            ry = _empty(T, dtype=_F32, device=where)
             a.rstd_y = ry.data_ptr()
-        if stats and pre_weight is not None:
-            rr = torch.empty(T, dtype=_F32, device=dev)
+        if pre_weight is not None:
+            rr = _empty(T, dtype=_F32, device=where)
             a.rstd_r = rr.data_ptr()
-        B.moe_norm_residual(a, st)
+    B.moe_norm_residual(a, _stream(dev))
     return NormForward(r, h, ry, rr)
 
 
@@ -278,40 +294,49 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
     dpost_weight, dpre_weight fp32 [D], dgate fp32 [D] / [T, 1] or [T, D] in the
     gate's type."""
     r = forward.r
-    dev = _cuda(r, "forward.r")
+    dev, dt = _input(r, "forward.r")
+    if (dh is not None) != (pre_weight is not None):
+        _bad("dh goes with pre_weight")
+    if post_weight is not None and forward.rstd_y is None or \
+            pre_weight is not None and forward.rstd_r is None:
+        _bad("forward ran without stats")
+    if dev != _device():
+        with _on(dev):
+            return norm_residual_backward(dr, dh, y, forward, post_weight=post_weight, gate=gate,
+                                          residual_scale=residual_scale, pre_weight=pre_weight)
     T, D = r.shape
-    _need((dh is not None) == (pre_weight is not None), "dh goes with pre_weight")
-    _need(post_weight is None or forward.rstd_y is not None, "forward ran without stats")
-    _need(pre_weight is None or forward.rstd_r is not None, "forward ran without stats")
-    _same(dev, dr=dr, dh=dh)
-    with _on(dev) as st:
-        a, keep = _norm_args(r.shape, r.dtype, dev, y, r, post_weight, gate, residual_scale,
-                             pre_weight, 1.0)
-        for n, t in (("dr", dr), ("dh", dh)):
-            if t is not None:
-                _need(t.shape == r.shape and t.dtype == r.dtype, f"{n} must have x's shape and type")
-                t, ld = _rows16(t)
-                setattr(a, n, t.data_ptr())
-                setattr(a, "ld" + n, ld)
-                keep.append(t)
-        a.rstd_y, a.rstd_r = _ptr(forward.rstd_y), _ptr(forward.rstd_r)
-        dx = torch.empty((T, D), dtype=r.dtype, device=dev)
-        dy = torch.empty((T, D), dtype=r.dtype, device=dev)
-        a.dx, a.lddx, a.dy, a.lddy = dx.data_ptr(), D, dy.data_ptr(), D
-        dpost = dpre = dgate = None
-        if post_weight is not None:
-            dpost = torch.empty(D, dtype=_F32, device=dev)
-            a.dpost_weight = dpost.data_ptr()
-        if pre_weight is not None:
-            dpre = torch.empty(D, dtype=_F32, device=dev)
-            a.dpre_weight = dpre.data_ptr()
-        if gate is not None:
-            full = a.gate_kind == B.MOE_GATE_FULL
-            dgate = torch.empty(gate.shape, dtype=r.dtype if full else _F32, device=dev)
-            a.dgate, a.lddg = dgate.data_ptr(), D
-        n = B.moe_norm_residual_workspace(T, D)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        B.moe_norm_residual_backward(a, _ptr(ws), n, st)
+    where, dtype = r.device, r.dtype
+    a, keep = _norm_args(T, D, dt, None, y, r, post_weight, gate, residual_scale, pre_weight, 1.0)
+    r, a.ldr = _rows16(r)
+    a.r = r.data_ptr()
+    if dr is not None:
+        _like(dr, "dr", dev, dtype, (T, D))
+        dr, a.lddr = _rows16(dr)
+        a.dr = dr.data_ptr()
+    dx = _empty(T, D, dtype=dtype, device=where)
+    dy = _empty(T, D, dtype=dtype, device=where)
+    a.dx, a.lddx, a.dy, a.lddy = dx.data_ptr(), D, dy.data_ptr(), D
+    dpost = dpre = dgate = None
+    if post_weight is not None:
+        _like(forward.rstd_y, "forward.rstd_y", dev, _F32, (T,))
+        a.rstd_y = forward.rstd_y.data_ptr()
+        dpost = _empty(D, dtype=_F32, device=where)
+        a.dpost_weight = dpost.data_ptr()
+    if pre_weight is not None:
+        _like(dh, "dh", dev, dtype, (T, D))
+        _like(forward.rstd_r, "forward.rstd_r", dev, _F32, (T,))
+        dh, a.lddh = _rows16(dh)
+        a.dh = dh.data_ptr()
+        a.rstd_r = forward.rstd_r.data_ptr()
+        dpre = _empty(D, dtype=_F32, device=where)
+        a.dpre_weight = dpre.data_ptr()
+    if gate is not None:
+        dgate = _empty(*gate.shape, dtype=dtype if a.gate_kind == B.MOE_GATE_FULL else _F32,
+                       device=where)
+        a.dgate, a.lddg = dgate.data_ptr(), D
+    n = B.moe_norm_residual_workspace(T, D)
+    ws = _empty(n, dtype=_U8, device=where)
+    B.moe_norm_residual_backward(a, ws.data_ptr(), n, _stream(dev))
     return NormBackward(dx, dy, dpost, dpre, dgate)
 
 
@@ -320,68 +345,75 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
 # ---------------------------------------------------------------------------
 def quantize_fp8(x, *, perm=None, k=1, relu2=False, transpose=False):
     """x [M, K] (fp32 or bf16) as E4M3 codes with a scale for each 128 of a row.
-    perm [R] int32: row r of the result is row perm[r] // k of x (zeros for a
-    negative entry).  relu2: of max(x, 0)^2.  transpose: of x's transpose, so
-    codes [K, M]."""
-    dev = _cuda(x, "x")
-    _need(x.dim() == 2, "x must be [M, K]")
-    dt = _dtype(x, "x")
+    perm [R] int32: row r of the result is row perm[r] // k of x (zeros for an
+    entry that names no row).  relu2: of max(x, 0)^2.  transpose: of x's
+    transpose, so codes [K, M]."""
+    dev, dt = _input(x, "x")
+    if dev != _device():
+        with _on(dev):
+            return quantize_fp8(x, perm=perm, k=k, relu2=relu2, transpose=transpose)
     M, K = x.shape
-    _need(not transpose or (perm is None and not relu2), "transpose takes neither perm nor relu2")
-    with _on(dev) as st:
-        x, ld = _rows(x)
-        if transpose:
-            codes = torch.empty((K, _up16(M)), dtype=_F8, device=dev)
-            scales = torch.empty((_blocks(M), K), dtype=_F32, device=dev)
-            B.moe_quantize_fp8_t(_ptr(x), dt, M, K, ld, _ptr(codes), codes.shape[1], _ptr(scales),
-                                 K, st)
-            return Fp8(codes[:, :M], scales)
-        R = M
-        if perm is not None:
-            _same(dev, perm=perm)
-            _need(perm.dim() == 1 and perm.dtype == _I32, "perm must be int32 [R]")
-            perm = perm.contiguous()
-            R = perm.shape[0]
-        codes = torch.empty((R, _up16(K)), dtype=_F8, device=dev)
-        scales = torch.empty((_blocks(K), R), dtype=_F32, device=dev)
-        B.moe_quantize_fp8(_ptr(x), dt, M, K, ld, _ptr(perm), R, k, int(relu2), _ptr(codes),
-                           codes.shape[1], _ptr(scales), R, st)
-    return Fp8(codes[:, :K], scales)
+    where = x.device
+    x, ld = _rows(x)
+    if transpose:
+        if perm is not None or relu2:
+            _bad("transpose takes neither perm nor relu2")
+        ldc = _up16(M)
+        codes = _empty(K, ldc, dtype=_F8, device=where)
+        scales = _empty(_blocks(M), K, dtype=_F32, device=where)
+        B.moe_quantize_fp8_t(x.data_ptr(), dt, M, K, ld, codes.data_ptr(), ldc, scales.data_ptr(),
+                             K, _stream(dev))
+        return Fp8(codes if ldc == M else codes[:, :M], scales)
+    R, at = M, None
+    if perm is not None:
+        if perm.dim() != 1 or perm.dtype != _I32 or perm.get_device() != dev:
+            _bad("perm must be int32 [R] on x's device")
+        perm = perm.contiguous()
+        R, at = perm.shape[0], perm.data_ptr()
+    ldc = _up16(K)
+    codes = _empty(R, ldc, dtype=_F8, device=where)
+    scales = _empty(_blocks(K), R, dtype=_F32, device=where)
+    B.moe_quantize_fp8(x.data_ptr(), dt, M, K, ld, at, R, k, 1 if relu2 else 0, codes.data_ptr(),
+                       ldc, scales.data_ptr(), R, _stream(dev))
+    return Fp8(codes if ldc == K else codes[:, :K], scales)
 
 
 def quantize_fp8_weight(w, *, transposed=False):
     """w [N, K] or [E, N, K] with a scale for each 128 x 128 block; with
     `transposed` also the transpose (of each matrix): (Fp8, Fp8)."""
-    dev = _cuda(w, "w")
-    _need(w.dim() in (2, 3), "w must be [N, K] or [E, N, K]")
-    dt = _dtype(w, "w")
+    dev, dt = _input(w, "w", 3 if isinstance(w, torch.Tensor) and w.dim() == 3 else 2)
+    if dev != _device():
+        with _on(dev):
+            return quantize_fp8_weight(w, transposed=transposed)
     lead = tuple(w.shape[:-2])
     N, K = w.shape[-2:]
-    with _on(dev) as st:
-        w = w.contiguous()
-        codes = torch.empty(lead + (N, _up16(K)), dtype=_F8, device=dev)
-        scales = torch.empty(lead + (_blocks(N), _blocks(K)), dtype=_F32, device=dev)
-        ct = sc = None
-        if transposed:
-            ct = torch.empty(lead + (K, _up16(N)), dtype=_F8, device=dev)
-            sc = torch.empty(lead + (_blocks(K), _blocks(N)), dtype=_F32, device=dev)
-        B.moe_quantize_fp8_weight(_ptr(w), dt, lead[0] if lead else 1, N, K, K, _ptr(codes),
-                                  _up16(K), _ptr(scales), _ptr(ct), _up16(N), _ptr(sc), st)
+    where = w.device
+    w = w.contiguous()
+    codes = _empty(*lead, N, _up16(K), dtype=_F8, device=where)
+    scales = _empty(*lead, _blocks(N), _blocks(K), dtype=_F32, device=where)
+    ct = sc = None
+    if transposed:
+        ct = _empty(*lead, K, _up16(N), dtype=_F8, device=where)
+        sc = _empty(*lead, _blocks(K), _blocks(N), dtype=_F32, device=where)
+    B.moe_quantize_fp8_weight(w.data_ptr(), dt, lead[0] if lead else 1, N, K, K, codes.data_ptr(),
+                              _up16(K), scales.data_ptr(), ct.data_ptr() if transposed else None,
+                              _up16(N), sc.data_ptr() if transposed else None, _stream(dev))
     q = Fp8(codes[..., :K], scales)
     return (q, Fp8(ct[..., :N], sc)) if transposed else q
 
 
 def _codes(t, what):
     """Codes whose rows are as the library reads them, and the row stride."""
-    _need(t.dtype in (_F8, torch.uint8), f"{what}.codes must be float8_e4m3fn or uint8")
-    ld, N = t.stride(-2), t.shape[-2]
-    ok = (t.stride(-1) == 1 or t.shape[-1] == 1) and ld % 16 == 0 and ld >= t.shape[-1] and \
-        t.data_ptr() % 16 == 0 and (t.dim() == 2 or t.stride(0) == N * ld or t.shape[0] == 1)
-    if not ok:
-        p = torch.empty(t.shape[:-1] + (_up16(t.shape[-1]),), dtype=t.dtype, device=t.device)
-        p[..., :t.shape[-1]] = t
-        t, ld = p, p.shape[-1]
-    return t, ld
+    if t.dtype != _F8 and t.dtype != _U8:
+        _bad(f"{what}.codes must be float8_e4m3fn or uint8")
+    st, N, K = t.stride(), t.shape[-2], t.shape[-1]
+    ld = st[-2] if N > 1 else max(_up16(K), st[-2])
+    if (st[-1] == 1 or K == 1) and not ld & 15 and ld >= K and not t.data_ptr() & 15 and \
+            (len(st) == 2 or st[0] == N * ld or t.shape[0] == 1):
+        return t, ld
+    p = _empty(*t.shape[:-1], _up16(K), dtype=t.dtype, device=t.device)
+    p[..., :K] = t
+    return p, p.shape[-1]
 
 
 def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
@@ -389,45 +421,50 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     weights [N, K], or rows [N, K] (the weight gradient).  With offsets [E + 1]
     int32 and b [E, N, K], rows [offsets[e], offsets[e + 1]) take b's matrix e;
     rows of `out` in no group keep their contents."""
-    dev = _cuda(a.codes, "a.codes")
-    _need(a.codes.dim() == 2, "a.codes must be [M, K]")
-    M, K = a.codes.shape
+    ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
+    if not (isinstance(ac, torch.Tensor) and ac.is_cuda):
+        _bad("a.codes must be a cuda tensor")
+    dev = ac.get_device()
+    if dev != _device():
+        with _on(dev):
+            return gemm_fp8(a, b, offsets=offsets, out_dtype=out_dtype, out=out)
+    if ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3):
+        _bad("a.codes must be [M, K] and b.codes [N, K], or [E, N, K] with offsets")
+    M, K = ac.shape
+    N = bc.shape[-2]
+    if bc.shape[-1] != K or bc.get_device() != dev:
+        _bad("b.codes must have a.codes' K and device")
     KB = _blocks(K)
-    _same(dev, a_scales=a.scales, b_codes=b.codes, b_scales=b.scales, offsets=offsets, out=out)
-    _need(a.scales.dtype == _F32 and a.scales.shape == (KB, M), "a.scales must be fp32 [ceil(K/128), M]")
-    grouped = offsets is not None
-    _need(b.codes.dim() == (3 if grouped else 2) and b.codes.shape[-1] == K,
-          "b.codes must be [N, K], or [E, N, K] with offsets")
-    N = b.codes.shape[-2]
-    lead = tuple(b.codes.shape[:-2])
-    _need(b.scales.dtype == _F32, "b.scales must be fp32")
+    _like(a_scales, "a.scales", dev, _F32, (KB, M))
+    if b_scales.dtype != _F32 or b_scales.get_device() != dev:
+        _bad("b.scales must be fp32 on a's device")
     # [NB, KB] and [KB, N] agree only at N = 1, K <= 128, where both are the one scale
-    weights = tuple(b.scales.shape) == lead + (_blocks(N), KB)
-    _need(weights or (not grouped and tuple(b.scales.shape) == (KB, N)),
-          "b.scales must be [.., ceil(N/128), ceil(K/128)], or [ceil(K/128), N]")
+    weights = b_scales.shape == (*bc.shape[:-2], _blocks(N), KB)
+    if not weights and (offsets is not None or b_scales.shape != (KB, N)):
+        _bad("b.scales must be [.., ceil(N/128), ceil(K/128)], or [ceil(K/128), N]")
     if out is None:
-        _need(out_dtype in _OUT, f"out_dtype must be one of {sorted(_OUT)}")
+        dtype = _OUT.get(out_dtype)
+        if dtype is None:
+            _bad(f"out_dtype must be one of {sorted(_OUT)}")
+        out = _empty(M, N, dtype=dtype, device=ac.device)
+    elif out.shape != (M, N) or out.dtype not in _CODE or out.get_device() != dev or \
+            out.stride(1) != 1 and N != 1 or out.stride(0) < N and M > 1:
+        _bad("out must be [M, N], fp32 or bf16, rows contiguous, on a's device")
+    ac, lda = _codes(ac, "a")
+    bc, ldb = _codes(bc, "b")
+    a_scales, lds = _rows(a_scales)
+    g = B.moe_fp8_gemm(M, N, K, 0, None, ac.data_ptr(), lda, a_scales.data_ptr(), lds,
+                       bc.data_ptr(), ldb, 0, 0, out.data_ptr(), max(out.stride(0), N),
+                       _CODE[out.dtype])
+    if weights:
+        b_scales = b_scales.contiguous()
     else:
-        _need(out.shape == (M, N) and out.dtype in _CODE and (out.stride(1) == 1 or N == 1)
-              and (out.stride(0) >= N or M <= 1), "out must be [M, N], rows contiguous")
-    with _on(dev) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=_OUT[out_dtype], device=dev)
-        ac, lda = _codes(a.codes, "a")
-        bc, ldb = _codes(b.codes, "b")
-        a_scales, lds = _rows(a.scales)
-        g = B.moe_fp8_gemm(M=M, N=N, K=K, a=_ptr(ac), lda=lda, a_scales=_ptr(a_scales),
-                           lda_scales=lds, b=_ptr(bc), ldb=ldb, out=_ptr(out),
-                           ldo=max(out.stride(0), N), out_dtype=_CODE[out.dtype])
-        if weights:
-            b_scales = b.scales.contiguous()
-        else:
-            b_scales, g.ldb_scales = _rows(b.scales)
-        g.b_scales = _ptr(b_scales)
-        if grouped:
-            _need(offsets.dtype == _I32 and offsets.shape == (lead[0] + 1,),
-                  "offsets must be int32 [E + 1]")
-            offsets = offsets.contiguous()
-            g.offsets, g.n_groups = _ptr(offsets), lead[0]
-        B.moe_gemm_fp8(g, st)
+        b_scales, g.ldb_scales = _rows(b_scales)
+    g.b_scales = b_scales.data_ptr()
+    if offsets is not None:
+        E = bc.shape[0]
+        _like(offsets, "offsets", dev, _I32, (E + 1,))
+        offsets = offsets.contiguous()
+        g.offsets, g.n_groups = offsets.data_ptr(), E
+    B.moe_gemm_fp8(g, _stream(dev))
     return out
