@@ -1208,11 +1208,11 @@ moe_status moe_sync(moe_handle* h, void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
   int word = 0;
   if (!h) {                      // the calls without a handle: fixed array, operators
-    int group = 0, gemm = 0;
+    int group = 0, gemm = 0, norm = 0;
     if (noalloc_take_error(&word) != cudaSuccess || route_group_take_error(&group) != cudaSuccess ||
-        fp8_gemm_take_error(&gemm) != cudaSuccess)
+        fp8_gemm_take_error(&gemm) != cudaSuccess || norm_take_error(&norm) != cudaSuccess)
       return MOE_ERR_CUDA;
-    word |= group | gemm;
+    word |= group | gemm | norm;
   } else {
     if (cudaMemcpy(&word, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
       return MOE_ERR_CUDA;

@@ -290,4 +290,5 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st);
 // the device error words of the calls without a handle: read, then cleared
 cudaError_t route_group_take_error(int* word);
 cudaError_t fp8_gemm_take_error(int* word);
+cudaError_t norm_take_error(int* word);
 }  // namespace lmoe

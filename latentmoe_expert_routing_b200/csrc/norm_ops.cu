@@ -16,13 +16,28 @@
 // splits, sum q y = sum (dr + rr v) b - rr^3 mean(v r) sum r b, so one block
 // reduction of three sums serves both means.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace lmoe {
 
 namespace {
 
+__device__ int g_norm_err;                    // DEV_ERR_TIMEOUT
+
 constexpr int kVec = 8;                       // elements per thread and step
+constexpr int kMaxStages = 4;
+constexpr int kMaxRing = 216 << 10;           // bytes of the backward's ring of rows
+
+// `bytes` contiguous bytes into shared memory, completion signalled on `bar`
+__device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(sm100::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes),
+        "r"(sm100::smem_u32(bar))
+      : "memory");
+}
 
 template <typename T> struct Pack;            // 8 elements as they lie in memory
 template <> struct Pack<__nv_bfloat16> {
@@ -43,6 +58,21 @@ template <> struct Pack<__nv_bfloat16> {
     for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
   }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // as four pairs
+  __device__ __forceinline__ void get2(uint64_t (&f)[4]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pack2(w[i] << 16, w[i] & 0xffff0000u);
+  }
+  __device__ __forceinline__ void set2(const uint64_t (&f)[4]) {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2(f[i], lo, hi);
+      h[i] = __floats2bfloat162_rn(lo, hi);
+    }
+  }
 };
 template <> struct Pack<float> {
   float4 a, b;
@@ -61,6 +91,12 @@ template <> struct Pack<float> {
   __device__ __forceinline__ void store(float* p) const {
     *reinterpret_cast<float4*>(p) = a;
     *reinterpret_cast<float4*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void get2(uint64_t (&f)[4]) const {
+    f[0] = pack2(a.x, a.y); f[1] = pack2(a.z, a.w); f[2] = pack2(b.x, b.y); f[3] = pack2(b.z, b.w);
+  }
+  __device__ __forceinline__ void set2(const uint64_t (&f)[4]) {
+    unpack2(f[0], a.x, a.y); unpack2(f[1], a.z, a.w); unpack2(f[2], b.x, b.y); unpack2(f[3], b.z, b.w);
   }
 };
 
@@ -95,7 +131,7 @@ __device__ __forceinline__ float rstd_of(float sum, int D, float eps) {
 }
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(512)
 norm_fwd_kernel(const moe_norm_args a) {
   __shared__ float s_red[2][32];
   const int D = a.D, nv = D / kVec;
@@ -181,132 +217,196 @@ norm_fwd_kernel(const moe_norm_args a) {
   }
 }
 
-// One block walks rows blockIdx.x, + gridDim.x, ...; thread i keeps the column
-// sums of its VPT vectors in registers and writes one partial row per block and
-// weight at the end (parts [3][grid][D]: post, pre, gate), which a second
-// kernel adds in block order.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024)
-norm_bwd_kernel(const moe_norm_args a, float* parts) {
+// One block walks rows blockIdx.x, + gridDim.x, ...  A row's inputs (y; r and dh;
+// dr; a full gate) arrive by bulk copies into a ring of rows in shared memory,
+// issued ahead by thread 0; the weights' vectors and the column sums stay in
+// registers.  A stage is refilled after the next row's block barrier, which
+// every thread reaches only when it is through with the stage.  Rows too long
+// for two stages are read from global memory directly (stages = 0).  What is
+// absent is filled in so that one formula serves: no w_post or gate is 1, no
+// w_pre is dh = r = 0.  At the end a block writes one partial row per kind of
+// column sum (parts [2][grid][D]), which a second kernel adds in block order.
+// Two sums per column are enough: with a channel gate dgate = w_post S and
+// dpost = g S, S = sum_t d y ry.
+//
+// Six rows of D move per row; an element costs about 17 instructions in packed
+// fp32 pairs (30 unpacked, which bounded the kernel).  T = D = 8192 bf16: NORM_BWD.
+template <typename T, int VPT, bool FULL>
+__global__ void __launch_bounds__(512)
+norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
+  extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_red[2][3 * 32];
+  __shared__ uint64_t s_full[kMaxStages];
+  constexpr bool kHold = VPT <= 2;                         // weights in registers
   const int D = a.D, nv = D / kVec;
-  const T* gate = static_cast<const T*>(a.gate);
+  const uint32_t row_bytes = D * sizeof(T);
   const T* wpost = static_cast<const T*>(a.post_weight);
   const T* wpre = static_cast<const T*>(a.pre_weight);
-  const bool gvec = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
-  // sums of d y ry (a channel gate: dgate and dpost are multiples of it), of
-  // d g y ry otherwise; and of dh r rr
-  float ca[VPT][8], cb[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ca[i][j] = cb[i][j] = 0.f;
-  int it = 0;
-  for (long row = blockIdx.x; row < a.T; row += gridDim.x, ++it) {
-    const T* y = static_cast<const T*>(a.y) + row * a.ldy;
-    const T* r = static_cast<const T*>(a.r) + row * a.ldr;
-    const T* dr = a.dr ? static_cast<const T*>(a.dr) + row * a.lddr : nullptr;
-    const T* dh = wpre ? static_cast<const T*>(a.dh) + row * a.lddh : nullptr;
-    const float ry = wpost ? a.rstd_y[row] : 1.f, rr = wpre ? a.rstd_r[row] : 0.f;
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(gate[row * a.ldg]) : 1.f;
-    Pack<T> py[VPT], pr[VPT], pd[VPT], ph[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      py[i].zero(); pr[i].zero(); pd[i].zero(); ph[i].zero();
-      if (v < nv) {
-        py[i].load(y + v * kVec);
-        if (dr) pd[i].load(dr + v * kVec);
-        if (wpre) { pr[i].load(r + v * kVec); ph[i].load(dh + v * kVec); }
-      }
+  const T* gvec = a.gate_kind == MOE_GATE_CHANNEL ? static_cast<const T*>(a.gate) : nullptr;
+  // a row's arrays, in this order: y, [r, dh], [dr], [gate]
+  const int n_dr = wpre ? 3 : 1, n_gate = n_dr + (a.dr != nullptr);
+  const uint32_t stage_bytes = (n_gate + FULL) * row_bytes;
+
+  auto source = [&](int k, long row) -> const T* {
+    if (k == 0) return static_cast<const T*>(a.y) + row * a.ldy;
+    if (wpre && k == 1) return static_cast<const T*>(a.r) + row * a.ldr;
+    if (wpre && k == 2) return static_cast<const T*>(a.dh) + row * a.lddh;
+    if (a.dr && k == n_dr) return static_cast<const T*>(a.dr) + row * a.lddr;
+    return static_cast<const T*>(a.gate) + row * a.ldg;
+  };
+  auto fetch = [&](long row, int st) {
+    sm100::mbar_arrive_expect_tx(&s_full[st], stage_bytes);
+    for (int k = 0; k < n_gate + FULL; ++k)
+      bulk_row(s_ring + (size_t)st * stage_bytes + k * row_bytes, source(k, row), row_bytes, &s_full[st]);
+  };
+  if (threadIdx.x == 0 && stages) {
+    for (int i = 0; i < stages; ++i) sm100::mbar_init(&s_full[i], 1);
+    sm100::fence_mbar_init();
+    sm100::fence_proxy_async();
+    for (int i = 0; i < stages; ++i) {
+      const long row = blockIdx.x + (long)i * gridDim.x;
+      if (row < a.T) fetch(row, i);
     }
+  }
+  const uint64_t one = both(1.f);
+  // w_pre, and w_post times a channel gate (ones where there is none)
+  auto weights = [&](int v, uint64_t (&we)[4], uint64_t (&wg)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) we[j] = wg[j] = one;
+    if (v >= nv) return;
+    Pack<T> p;
+    if (wpre) { p.load(wpre + v * kVec); p.get2(we); }
+    if (wpost) { p.load(wpost + v * kVec); p.get2(wg); }
+    if (gvec) {
+      uint64_t g[4];
+      p.load(gvec + v * kVec);
+      p.get2(g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wg[j] = mul2(wg[j], g[j]);
+    }
+  };
+  uint64_t we_[kHold ? VPT : 1][4], wg_[kHold ? VPT : 1][4], ca[VPT][4], cb[VPT][4];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    if constexpr (kHold) weights(threadIdx.x + i * blockDim.x, we_[i], wg_[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ca[i][j] = cb[i][j] = 0;
+  }
+  auto scalars = [&](long row, float& ry, float& rr, float& gt) {
+    ry = wpost ? a.rstd_y[row] : 1.f;
+    rr = wpre ? a.rstd_r[row] : 0.f;
+    gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 1.f;
+  };
+  float ry, rr, gt;
+  scalars(blockIdx.x, ry, rr, gt);
+  __syncthreads();                                         // the barriers exist
+  int st = 0, phase = 0, it = 0;
+  for (long row = blockIdx.x; row < a.T; row += gridDim.x, it ^= 1) {
+    // a bulk copy that never lands is reported, not waited for without end
+    if (stages && !sm100::mbar_wait(&s_full[st], phase)) atomicOr(&g_norm_err, DEV_ERR_TIMEOUT);
+    const T* ring = reinterpret_cast<const T*>(s_ring + (size_t)st * stage_bytes);
+    // vector v of the row's array k
+    auto get = [&](int k, int v, uint64_t (&f)[4]) {
+      Pack<T> p;
+      p.load((stages ? ring + (size_t)k * D : source(k, row)) + v * kVec);
+      p.get2(f);
+    };
+    // r, dh and dr of vector v (zeros where absent), y, the weights; with a full
+    // gate wg is w_post times it
+    auto vector = [&](int i, int v, uint64_t (&fr)[4], uint64_t (&fh)[4], uint64_t (&fd)[4],
+                      uint64_t (&fy)[4], uint64_t (&we)[4], uint64_t (&wg)[4], uint64_t (&g)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fr[j] = fh[j] = fd[j] = 0;
+      get(0, v, fy);
+      if (wpre) { get(1, v, fr); get(2, v, fh); }
+      if (a.dr) get(n_dr, v, fd);
+      if constexpr (kHold) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { we[j] = we_[i][j]; wg[j] = wg_[i][j]; }
+      } else {
+        weights(v, we, wg);
+      }
+      if constexpr (FULL) {
+        get(n_gate, v, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wg[j] = mul2(wg[j], g[j]);
+      }
+    };
     // sum v r; sum (dr + rr v) b; sum r b, with b = w_post y [gate vector]
-    float s[3] = {0.f, 0.f, 0.f};
+    uint64_t s0 = 0, s1 = 0, s2 = 0;
+    const uint64_t rr2 = both(rr);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nv) continue;
-      float fy[8], fr[8], fd[8], fh[8], w[8];
-      Pack<T> p;
-      py[i].get(fy); pr[i].get(fr); pd[i].get(fd); ph[i].get(fh);
-      if (wpre) {
-        p.load(wpre + v * kVec);
-        p.get(w);
+      uint64_t fr[4], fh[4], fd[4], fy[4], we[4], wg[4], g[4];
+      vector(i, v, fr, fh, fd, fy, we, wg, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          fh[j] *= w[j];
-          s[0] = fmaf(fh[j], fr[j], s[0]);
-          fd[j] = fmaf(rr, fh[j], fd[j]);
-        }
-      }
-      if (wpost) {
-        p.load(wpost + v * kVec);
-        p.get(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) fy[j] *= w[j];
-      }
-      if (gvec) {
-        p.load(gate + (a.gate_kind == MOE_GATE_FULL ? row * a.ldg : 0) + v * kVec);
-        p.get(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) fy[j] *= w[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[1] = fmaf(fd[j], fy[j], s[1]);
-        s[2] = fmaf(fr[j], fy[j], s[2]);
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t vv = mul2(fh[j], we[j]), b = mul2(fy[j], wg[j]);
+        s0 = fma2(vv, fr[j], s0);
+        s1 = fma2(fma2(rr2, vv, fd[j]), b, s1);
+        s2 = fma2(fr[j], b, s2);
       }
     }
-    block_sum<3>(s, s_red[it & 1]);
+    float s[3], hi;
+    unpack2(s0, s[0], hi); s[0] += hi;
+    unpack2(s1, s[1], hi); s[1] += hi;
+    unpack2(s2, s[2], hi); s[2] += hi;
+    block_sum<3>(s, s_red[it]);
+    if (threadIdx.x == 0 && stages && row >= (long)gridDim.x) {          // the last row's stage
+      const long next = row + (long)(stages - 1) * gridDim.x;
+      if (next < a.T) fetch(next, st ? st - 1 : stages - 1);
+    }
     const float m1 = rr * rr * rr * (s[0] / (float)D);     // d = dr + rr v - m1 r
     const float dot = s[1] - m1 * s[2];                    // sum d b
     const float m2 = wpost ? ry * ry * ry * gt * (dot / (float)D) : 0.f;
     if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0)
       static_cast<float*>(a.dgate)[row] = ry * dot;
+    const uint64_t m12 = both(-m1), m22 = both(-m2), ry2 = both(ry), gt2 = both(gt),
+                   rg2 = both(ry * gt), al2 = both(a.residual_scale);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
     T* dy = static_cast<T*>(a.dy) + row * a.lddy;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nv) continue;
-      float fy[8], fr[8], d[8], f[8], w[8], g[8];
+      uint64_t fr[4], fh[4], d[4], fy[4], we[4], wg[4], g[4];
+      vector(i, v, fr, fh, d, fy, we, wg, g);
       Pack<T> p;
-      py[i].get(fy); pr[i].get(fr); pd[i].get(d); ph[i].get(f);
-      if (wpre) {
-        p.load(wpre + v * kVec);
-        p.get(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          cb[i][j] = fmaf(f[j] * rr, fr[j], cb[i][j]);
-          d[j] = fmaf(rr, f[j] * w[j], d[j]) - m1 * fr[j];
-        }
+      for (int j = 0; j < 4; ++j) {
+        fh[j] = mul2(fh[j], rr2);
+        cb[i][j] = fma2(fh[j], fr[j], cb[i][j]);
+        d[j] = fma2(m12, fr[j], fma2(fh[j], we[j], d[j]));
+        fr[j] = mul2(al2, d[j]);
+        fh[j] = mul2(fy[j], ry2);                          // y ry
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = a.residual_scale * d[j];
-      p.set(f);
+      p.set2(fr);
       p.store(dx + v * kVec);
+      if constexpr (FULL) {
+        uint64_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) { g[j] = gt; w[j] = 1.f; }
-      if (gvec) {
-        p.load(gate + (a.gate_kind == MOE_GATE_FULL ? row * a.ldg : 0) + v * kVec);
-        p.get(g);
-      }
-      if (wpost) { p.load(wpost + v * kVec); p.get(w); }
-      if (a.gate_kind == MOE_GATE_FULL) {
+        for (int j = 0; j < 4; ++j) w[j] = one;
+        if (wpost) { Pack<T> q; q.load(wpost + v * kVec); q.get2(w); }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = d[j] * fy[j] * ry * w[j];
-        p.set(f);
+        for (int j = 0; j < 4; ++j) fr[j] = mul2(mul2(d[j], fh[j]), w[j]);
+        p.set2(fr);
         p.store(static_cast<T*>(a.dgate) + row * a.lddg + v * kVec);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fh[j] = mul2(fh[j], g[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dn = d[j] * g[j];
-        ca[i][j] = fmaf(a.gate_kind == MOE_GATE_CHANNEL ? d[j] : dn, fy[j] * ry, ca[i][j]);
-        f[j] = wpost ? fmaf(ry, dn * w[j], -m2 * fy[j]) : dn;
+      for (int j = 0; j < 4; ++j) {
+        // S of a channel gate; otherwise the gate (gt, g) belongs to dpost's sum
+        ca[i][j] = fma2(mul2(d[j], gt2), fh[j], ca[i][j]);
+        fr[j] = fma2(m22, fy[j], mul2(mul2(d[j], wg[j]), rg2));
       }
-      p.set(f);
+      p.set2(fr);
       p.store(dy + v * kVec);
     }
+    if (stages && ++st == stages) { st = 0; phase ^= 1; }
+    scalars(min(row + (long)gridDim.x, (long)a.T - 1), ry, rr, gt);       // the next row's
   }
   // partial column sums of this block
   const size_t plane = (size_t)gridDim.x * D;
@@ -314,13 +414,12 @@ norm_bwd_kernel(const moe_norm_args a, float* parts) {
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nv) continue;
-    float* o = parts + (size_t)blockIdx.x * D + v * kVec;
-    *reinterpret_cast<float4*>(o) = make_float4(ca[i][0], ca[i][1], ca[i][2], ca[i][3]);
-    *reinterpret_cast<float4*>(o + 4) = make_float4(ca[i][4], ca[i][5], ca[i][6], ca[i][7]);
+    Pack<float> p;
+    p.set2(ca[i]);
+    p.store(parts + (size_t)blockIdx.x * D + v * kVec);
     if (wpre) {
-      o += plane;
-      *reinterpret_cast<float4*>(o) = make_float4(cb[i][0], cb[i][1], cb[i][2], cb[i][3]);
-      *reinterpret_cast<float4*>(o + 4) = make_float4(cb[i][4], cb[i][5], cb[i][6], cb[i][7]);
+      p.set2(cb[i]);
+      p.store(parts + plane + (size_t)blockIdx.x * D + v * kVec);
     }
   }
 }
@@ -355,47 +454,102 @@ norm_bwd_reduce_kernel(const moe_norm_args a, const float* __restrict__ parts, i
   if (a.post_weight) static_cast<float*>(a.dpost_weight)[col] = va;
 }
 
-// threads and vectors per thread for D / 8 vectors
-struct Shape { int threads, vpt; };
-Shape shape_for(int D, int want) {
-  const int nv = D / kVec;
-  int vpt = want;
-  while (ceil_div(nv, vpt) > 1024) vpt *= 2;
-  return {(ceil_div(nv, vpt) + 31) / 32 * 32, vpt};
-}
-
+// Forward: about 256 threads a row, so that several rows are under way on an SM
+// (D = 8192: 128 -> 94 us at 8192 rows against 1024 threads); with fewer rows
+// than that fills, as many threads as the row has vectors (64 rows: 5.8 -> 4.2 us).
 template <typename T>
 cudaError_t fwd_t(const moe_norm_args& a, cudaStream_t st) {
-  const Shape s = shape_for(a.D, 1);
-  if (s.vpt == 1) norm_fwd_kernel<T, 1><<<a.T, s.threads, 0, st>>>(a);
-  else norm_fwd_kernel<T, 2><<<a.T, s.threads, 0, st>>>(a);
+  const int nv = a.D / kVec;
+  const int vpt = a.T <= 296 ? (nv <= 512 ? 1 : nv <= 1024 ? 2 : 4) : nv <= 256 ? 1 : nv <= 512 ? 2 : 4;
+  const int threads = (ceil_div(nv, vpt) + 31) / 32 * 32;
+  if (vpt == 1) norm_fwd_kernel<T, 1><<<a.T, threads, 0, st>>>(a);
+  else if (vpt == 2) norm_fwd_kernel<T, 2><<<a.T, threads, 0, st>>>(a);
+  else norm_fwd_kernel<T, 4><<<a.T, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd_t(const moe_norm_args& a, float* ws, int nblk, cudaStream_t st) {
-  const Shape s = shape_for(a.D, 1);
-  if (s.vpt == 1) norm_bwd_kernel<T, 1><<<nblk, s.threads, 0, st>>>(a, ws);
-  else norm_bwd_kernel<T, 2><<<nblk, s.threads, 0, st>>>(a, ws);
-  if (a.post_weight || a.pre_weight || a.gate_kind == MOE_GATE_CHANNEL)
-    norm_bwd_reduce_kernel<T><<<ceil_div(a.D, 32), 1024, 0, st>>>(a, ws, nblk);
+// Backward: vectors per thread, threads, blocks per SM and ring stages.  Two
+// vectors a thread (four past 1024 vectors, so that a block has at most 512
+// threads) keep the weights and sums in registers; the SM's shared memory is
+// shared out over enough blocks for 512 threads.
+struct BwdShape { int vpt, threads, blocks, stages; size_t smem; };
+BwdShape bwd_shape(const moe_norm_args& a) {
+  BwdShape s;
+  const int nv = a.D / kVec, es = a.dtype == MOE_BF16 ? 2 : 4;
+  s.vpt = nv <= 256 ? 1 : nv <= 1024 ? 2 : 4;
+  s.threads = (ceil_div(nv, s.vpt) + 31) / 32 * 32;
+  int per_sm = 512 / s.threads;
+  per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+  const int arrays = 1 + (a.pre_weight ? 2 : 0) + (a.dr ? 1 : 0) + (a.gate_kind == MOE_GATE_FULL ? 1 : 0);
+  const size_t row = (size_t)arrays * a.D * es, room = size_t(216) << 10;
+  const size_t n = room / per_sm / row;
+  s.stages = n < 2 ? 0 : n > kMaxStages ? kMaxStages : (int)n;
+  s.smem = row * s.stages;
+  const long blocks = 148L * per_sm;
+  s.blocks = (int)(a.T < blocks ? a.T : blocks);
+  return s;
+}
+
+template <typename T, int VPT, bool FULL>
+cudaError_t bwd_v(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStream_t st) {
+  auto kern = norm_bwd_kernel<T, VPT, FULL>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing)) != cudaSuccess)
+      return e;
+    configured[dev] = true;
+  }
+  kern<<<s.blocks, s.threads, s.smem, st>>>(a, ws, s.stages);
   return cudaGetLastError();
+}
+
+template <typename T, bool FULL>
+cudaError_t bwd_f(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStream_t st) {
+  return s.vpt == 1 ? bwd_v<T, 1, FULL>(a, s, ws, st)
+       : s.vpt == 2 ? bwd_v<T, 2, FULL>(a, s, ws, st) : bwd_v<T, 4, FULL>(a, s, ws, st);
+}
+
+template <typename T>
+cudaError_t bwd_t(const moe_norm_args& a, float* ws, cudaStream_t st) {
+  const BwdShape s = bwd_shape(a);
+  cudaError_t e = a.gate_kind == MOE_GATE_FULL ? bwd_f<T, true>(a, s, ws, st)
+                                               : bwd_f<T, false>(a, s, ws, st);
+  if (e == cudaSuccess && (a.post_weight || a.pre_weight || a.gate_kind == MOE_GATE_CHANNEL)) {
+    norm_bwd_reduce_kernel<T><<<ceil_div(a.D, 32), 1024, 0, st>>>(a, ws, s.blocks);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
 
-int norm_bwd_blocks(int T) { return T < 296 ? T : 296; }
+// two partial rows for each block of any shape
+size_t norm_bwd_workspace(int T, int D) {
+  const int nv = D / kVec, threads = (ceil_div(nv, nv <= 256 ? 1 : nv <= 1024 ? 2 : 4) + 31) / 32 * 32;
+  int per_sm = 512 / threads;
+  per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+  const long blocks = 148L * per_sm;
+  return (size_t)2 * (T < blocks ? T : blocks) * D * 4;
+}
 
-size_t norm_bwd_workspace(int T, int D) { return (size_t)2 * norm_bwd_blocks(T) * D * 4; }
+cudaError_t norm_take_error(int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_norm_err, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_norm_err, &zero, sizeof(int));
+  return e;
+}
 
 cudaError_t launch_norm_fwd(const moe_norm_args& a, cudaStream_t st) {
   return a.dtype == MOE_BF16 ? fwd_t<__nv_bfloat16>(a, st) : fwd_t<float>(a, st);
 }
 
 cudaError_t launch_norm_bwd(const moe_norm_args& a, void* ws, cudaStream_t st) {
-  const int nblk = norm_bwd_blocks(a.T);
-  return a.dtype == MOE_BF16 ? bwd_t<__nv_bfloat16>(a, static_cast<float*>(ws), nblk, st)
-                             : bwd_t<float>(a, static_cast<float*>(ws), nblk, st);
+  return a.dtype == MOE_BF16 ? bwd_t<__nv_bfloat16>(a, static_cast<float*>(ws), st)
+                             : bwd_t<float>(a, static_cast<float*>(ws), st);
 }
 
 }  // namespace lmoe

@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "pair_sm100.cuh"
 #include "sm100.cuh"
@@ -429,26 +430,6 @@ struct WCfg {
   }
 };
 
-// two fp32 fused multiply-adds / products in one instruction
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 __device__ __forceinline__ void mma_pair_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
@@ -652,7 +633,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           break;
         }
         tc_fence_after();
-        const uint64_t rs2 = pack2(__float_as_uint(rs), __float_as_uint(rs));
+        const uint64_t rs2 = both(rs);
         const float* cs = s_scale + ss * C::kScaleFloats + c0;
 #pragma unroll
         for (int c = 0; c < kWCols; c += 64) {
