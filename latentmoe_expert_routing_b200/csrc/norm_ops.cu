@@ -231,7 +231,7 @@ norm_fwd_kernel(const moe_norm_args a) {
 //
 // Six rows of D move per row; an element costs about 17 instructions in packed
 // fp32 pairs (30 unpacked, which bounded the kernel).  T = D = 8192 bf16: NORM_BWD.
-template <typename T, int VPT, bool FULL>
+template <typename T, int VPT, bool FULL, bool RING>
 __global__ void __launch_bounds__(512)
 norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
   extern __shared__ __align__(16) uint8_t s_ring[];
@@ -259,7 +259,7 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
     for (int k = 0; k < n_gate + FULL; ++k)
       bulk_row(s_ring + (size_t)st * stage_bytes + k * row_bytes, source(k, row), row_bytes, &s_full[st]);
   };
-  if (threadIdx.x == 0 && stages) {
+  if (RING && threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) sm100::mbar_init(&s_full[i], 1);
     sm100::fence_mbar_init();
     sm100::fence_proxy_async();
@@ -303,12 +303,13 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
   int st = 0, phase = 0, it = 0;
   for (long row = blockIdx.x; row < a.T; row += gridDim.x, it ^= 1) {
     // a bulk copy that never lands is reported, not waited for without end
-    if (stages && !sm100::mbar_wait(&s_full[st], phase)) atomicOr(&g_norm_err, DEV_ERR_TIMEOUT);
+    if (RING && !sm100::mbar_wait(&s_full[st], phase)) atomicOr(&g_norm_err, DEV_ERR_TIMEOUT);
     const T* ring = reinterpret_cast<const T*>(s_ring + (size_t)st * stage_bytes);
     // vector v of the row's array k
     auto get = [&](int k, int v, uint64_t (&f)[4]) {
       Pack<T> p;
-      p.load((stages ? ring + (size_t)k * D : source(k, row)) + v * kVec);
+      if constexpr (RING) p.load(ring + k * D + v * kVec);
+      else p.load(source(k, row) + v * kVec);
       p.get2(f);
     };
     // r, dh and dr of vector v (zeros where absent), y, the weights; with a full
@@ -354,7 +355,7 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
     unpack2(s1, s[1], hi); s[1] += hi;
     unpack2(s2, s[2], hi); s[2] += hi;
     block_sum<3>(s, s_red[it]);
-    if (threadIdx.x == 0 && stages && row >= (long)gridDim.x) {          // the last row's stage
+    if (RING && threadIdx.x == 0 && row >= (long)gridDim.x) {          // the last row's stage
       const long next = row + (long)(stages - 1) * gridDim.x;
       if (next < a.T) fetch(next, st ? st - 1 : stages - 1);
     }
@@ -405,7 +406,7 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
       p.set2(fr);
       p.store(dy + v * kVec);
     }
-    if (stages && ++st == stages) { st = 0; phase ^= 1; }
+    if (RING && ++st == stages) { st = 0; phase ^= 1; }
     scalars(min(row + (long)gridDim.x, (long)a.T - 1), ry, rr, gt);       // the next row's
   }
   // partial column sums of this block
@@ -490,9 +491,9 @@ BwdShape bwd_shape(const moe_norm_args& a) {
   return s;
 }
 
-template <typename T, int VPT, bool FULL>
+template <typename T, int VPT, bool FULL, bool RING>
 cudaError_t bwd_v(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStream_t st) {
-  auto kern = norm_bwd_kernel<T, VPT, FULL>;
+  auto kern = norm_bwd_kernel<T, VPT, FULL, RING>;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -509,8 +510,9 @@ cudaError_t bwd_v(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStre
 
 template <typename T, bool FULL>
 cudaError_t bwd_f(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStream_t st) {
-  return s.vpt == 1 ? bwd_v<T, 1, FULL>(a, s, ws, st)
-       : s.vpt == 2 ? bwd_v<T, 2, FULL>(a, s, ws, st) : bwd_v<T, 4, FULL>(a, s, ws, st);
+  if (s.vpt == 1) return bwd_v<T, 1, FULL, true>(a, s, ws, st);    // at most 2048 columns
+  if (s.stages) return s.vpt == 2 ? bwd_v<T, 2, FULL, true>(a, s, ws, st) : bwd_v<T, 4, FULL, true>(a, s, ws, st);
+  return s.vpt == 2 ? bwd_v<T, 2, FULL, false>(a, s, ws, st) : bwd_v<T, 4, FULL, false>(a, s, ws, st);
 }
 
 template <typename T>
