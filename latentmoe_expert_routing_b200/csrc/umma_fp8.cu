@@ -102,28 +102,35 @@ __device__ __forceinline__ void arrive_tmem(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+
+constexpr int kScaleSteps = 4;             // steps per slot of the tall form's scale ring
 
 template <int NT>
 struct TCfg {
   static constexpr int kQBytes = NT * kKB;
   static constexpr int kStageBytes = kPBytes + kQBytes;
   static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
-  static constexpr int kWarps = 4;                              // promoting warps
-  static constexpr int kThreads = 64 + 32 * kWarps;
-  static constexpr int kScaleFloats = 4 + NT;                   // the block's, then the columns'
-  static constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kBufs = NT <= 64 ? 4 : 2;                // partial sums in TMEM
+  static constexpr int kSlots = 3;
+  static constexpr int kThreads = 256;
+  static constexpr int kStepFloats = NT;                        // the columns' scale products
+  static constexpr uint32_t kTmemCols = kBufs * NT;             // two CTAs share an SM's 512
   static constexpr int kScaleOffset = kStages * kStageBytes;
-  static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
+  static constexpr int kBarOffset = kScaleOffset + kSlots * kScaleSteps * kStepFloats * 4;
   static constexpr int kTableOffset = kBarOffset + 512;
   static constexpr int bytes(int groups) {         // groups: 0 for a plain product
     return kTableOffset + (groups ? 2 * (groups + 1) * 4 : 0) + 1024;
   }
 };
+// registers: the launch gives 256 x 128; the first warpgroup keeps 40 a thread, which
+// leaves the promoting one 216
+constexpr int kTRegsLow = 40, kTRegsHigh = 216;
 
 struct Tile {
   int grp;
@@ -213,12 +220,11 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_scale = reinterpret_cast<float*>(smem + C::kScaleOffset);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* sfull = empty + C::kStages;
-  uint64_t* sempty = sfull + kScaleRing;
-  uint64_t* tfull = sempty + kScaleRing;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* mma_done = tempty + 2;
+  uint64_t* done = full + C::kStages;             // a step's products are finished
+  uint64_t* sfull = done + C::kStages;
+  uint64_t* sempty = sfull + C::kSlots;
+  uint64_t* tempty = sempty + C::kSlots;
+  uint64_t* mma_done = tempty + C::kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_tiles = reinterpret_cast<int*>(smem + C::kTableOffset);
@@ -229,10 +235,10 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
   const uint32_t rank = split > 1 ? pair2::cluster_rank() : 0u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int s = 0; s < kScaleRing; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], C::kWarps); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], C::kWarps); }
-    mbar_init(mma_done, 1);
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&done[s], 1); }
+    for (int s = 0; s < C::kSlots; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], 4); }
+    for (int b = 0; b < C::kBufs; ++b) mbar_init(&tempty[b], 4);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&amap);
@@ -253,119 +259,149 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     *abort_flag = 1;
   };
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
-      Tile ti;
-      if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
-      const int brow = ti.grp * a.N + ti.n0;
-      const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t st = it % C::kStages, ss = it % kScaleRing;
-        ok = mbar_wait(&empty[st], ((it / C::kStages) & 1) ^ 1) &&
-             mbar_wait(&sempty[ss], ((it / kScaleRing) & 1) ^ 1);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[st], C::kStageBytes);
-          uint8_t* sp = smem + st * C::kStageBytes;
-          tma_load_2d(sp, &bmap, &full[st], kb * kKB, brow);
-          tma_load_2d(sp + kPBytes, &amap, &full[st], kb * kKB, ti.m0);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsLow));
+    if (warp == 0) {
+      // ---------------- tiles by TMA ----------------
+      if (lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+          Tile ti;
+          if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
+          const int brow = ti.grp * a.N + ti.n0;
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const uint32_t st = it % C::kStages;
+            if (!mbar_wait(&done[st], ((it / C::kStages) & 1) ^ 1)) { ok = false; fail(); break; }
+            mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+            uint8_t* sp = smem + st * C::kStageBytes;
+            tma_load_2d(sp, &bmap, &full[st], kb * kKB, brow);
+            tma_load_2d(sp + kPBytes, &amap, &full[st], kb * kKB, ti.m0);
+          }
         }
-        float* sc = s_scale + ss * C::kScaleFloats;
-        const float* sa = a.sa + (size_t)kb * a.ldsa + ti.m0;
-        if (lane == 0) cp_async4(sc, sb + kb, true);
-        for (int i = lane; i < NT; i += 32) cp_async4(sc + 4 + i, sa + (i < ti.rows ? i : 0), i < ti.rows);
-        cp_async_arrive(&sfull[ss]);
+        // nothing may be in flight into this CTA's memory when it ends
+        const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+        for (uint32_t j = 0; j < n && ok; ++j) {
+          const uint32_t i = it - 1 - j;
+          if (!mbar_wait(&done[i % C::kStages], (i / C::kStages) & 1)) { ok = false; fail(); }
+        }
+        if (!ok)
+          for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t i = it - 1 - j;
+            mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1);
+          }
       }
-    }
-    // nothing may be in flight into this CTA's memory when it ends
-    const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
-    for (uint32_t j = 0; j < n && ok; ++j) {
-      const uint32_t i = it - 1 - j;
-      if (!mbar_wait(&empty[i % C::kStages], (i / C::kStages) & 1)) { ok = false; fail(); }
-    }
-    if (!ok) {
-      // an abandoned pipeline: wait (bounded) for the loads themselves
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint32_t i = it - 1 - j;
-        mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- scale products, kScaleSteps steps at a time ----------------
+      uint32_t sl = 0;
+      bool ok = true;
+      for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+        Tile ti;
+        if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
+        const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB;
+        const float* sa = a.sa + (size_t)kb0 * a.ldsa + ti.m0;
+        constexpr int PL = (NT + 31) / 32;                 // columns per lane
+        for (int kb = kb0; kb < kb1; kb += kScaleSteps, ++sl) {
+          const uint32_t ss = sl % C::kSlots;
+          float v[kScaleSteps][PL];
+#pragma unroll
+          for (int k = 0; k < kScaleSteps; ++k, sa += a.ldsa) {
+            const bool in = kb + k < kb1;
+            const float bs = in ? __ldg(sb + kb + k) : 0.f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+              v[k][i] = in && lane + 32 * i < ti.rows ? __ldg(sa + lane + 32 * i) * bs : 0.f;
+          }
+          ok = mbar_wait(&sempty[ss], ((sl / C::kSlots) & 1) ^ 1);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+          float* sc = s_scale + ss * kScaleSteps * C::kStepFloats;
+#pragma unroll
+          for (int k = 0; k < kScaleSteps; ++k)
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+              if (lane + 32 * i < NT) sc[k * NT + lane + 32 * i] = v[k][i];
+          mbar_arrive(&sfull[ss]);
+        }
       }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    } else if (lane == 0) {
+      // ---------------- MMA issuers: warp 1 the even steps, warp 3 the odd ones ----------------
+      const uint32_t odd = warp >> 1;
       const uint64_t desc0 = sw128_desc(smem_u32(smem));
       uint32_t it = 0;
       bool ok = true;
       for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
         Tile ti;
-        if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
+        if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
         const uint32_t idesc = idesc_f8(kRowsP, (ti.rows + 15) & ~15);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t st = it % C::kStages, b = it & 1;
-          if (!mbar_wait(&tempty[b], ((it >> 1) & 1) ^ 1) ||
-              !mbar_wait(&full[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
-          tc_fence_after();
+        const uint32_t end = it + (kb1 - kb0);
+        for (it += (it ^ odd) & 1; it < end; it += 2) {
+          const uint32_t st = it % C::kStages, b = it % C::kBufs;
           const uint64_t pd = desc0 + (uint64_t)(st * (C::kStageBytes >> 4));
           const uint64_t qd = pd + (uint64_t)(kPBytes >> 4);
-          const uint32_t d = tmem + b * NT;
+          if (!mbar_wait(&tempty[b], ((it / C::kBufs) & 1) ^ 1) ||
+              !mbar_wait(&full[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
+          tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f8_ss(d, pd + 2 * k, qd + 2 * k, idesc, k > 0);
-          mma_commit(&empty[st]);
-          mma_commit(&tfull[b]);
+          for (int k = 0; k < 4; ++k) mma_f8_ss(tmem + b * NT, pd + 2 * k, qd + 2 * k, idesc, k > 0);
+          mma_commit(&done[st]);
         }
+        it = end;
       }
       mma_commit(mma_done);                  // nothing may write TMEM once it is freed
       if (!mbar_wait(mma_done, 0)) fail();
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsHigh));
     // ---------------- promotion and store ----------------
     const int q = warp & 3;                                // TMEM lane quarter
     const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
     const int prow = 32 * q + lane;                        // this thread's weight row
-    constexpr int kChunk = NT == 16 || NT == 128 ? 16 : 32;   // 128 sums leave no room for 32
-    uint32_t it = 0;
+    constexpr int kChunk = NT < 64 ? NT : 64;
+    uint32_t it = 0, sl = 0;
     bool ok = true;
     TO* out = static_cast<TO*>(a.out);
     for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
       Tile ti;
-      if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) continue;
-      float acc[NT];
+      if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
+      uint64_t acc[NT / 2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j] = 0.f;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t ss = it % kScaleRing, b = it & 1;
-        if (!mbar_wait(&sfull[ss], (it / kScaleRing) & 1) || !mbar_wait(&tfull[b], (it >> 1) & 1)) {
-          ok = false;
-          fail();
-          break;
-        }
-        tc_fence_after();
-        const float* sc = s_scale + ss * C::kScaleFloats;
-        const float bs = sc[0];
+      for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
+      for (int kb = kb0; kb < kb1 && ok; kb += kScaleSteps, ++sl) {
+        const uint32_t ss = sl % C::kSlots;
+        if (!mbar_wait(&sfull[ss], (sl / C::kSlots) & 1)) { ok = false; fail(); break; }
+        const float* sc = s_scale + ss * kScaleSteps * C::kStepFloats;
+        const int steps = min(kScaleSteps, kb1 - kb);
+        for (int k = 0; k < steps; ++k, ++it, sc += C::kStepFloats) {
+          const uint32_t st = it % C::kStages, b = it % C::kBufs;
+          if (!mbar_wait(&done[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < NT; c += kChunk) {
-          if (c >= ti.rows) break;                         // uniform in the warp
-          uint32_t r[kChunk];
-          if constexpr (kChunk == 32) pair2::tmem_ld32(tbase + b * NT + c, r);
-          else tmem_ld16(tbase + b * NT + c, r);
-          tmem_ld_wait();
+          for (int c = 0; c < NT; c += kChunk) {
+            if (c >= ti.rows) break;                       // uniform in the warp
+            uint32_t r[kChunk];
+            if constexpr (kChunk == 16) {
+              tmem_ld16(tbase + b * NT + c, r);
+            } else {
 #pragma unroll
-          for (int j = 0; j < kChunk; j += 4) {
-            const float4 cs = *reinterpret_cast<const float4*>(sc + 4 + c + j);
-            acc[c + j] = fmaf(__uint_as_float(r[j]), bs * cs.x, acc[c + j]);
-            acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), bs * cs.y, acc[c + j + 1]);
-            acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), bs * cs.z, acc[c + j + 2]);
-            acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), bs * cs.w, acc[c + j + 3]);
+              for (int h = 0; h < kChunk; h += 32)
+                pair2::tmem_ld32(tbase + b * NT + c + h, *reinterpret_cast<uint32_t(*)[32]>(r + h));
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < kChunk; j += 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(sc + c + j);
+              uint64_t* s = &acc[(c + j) >> 1];
+              s[0] = fma2(pack2(r[j], r[j + 1]), pack2(w.x, w.y), s[0]);
+              s[1] = fma2(pack2(r[j + 2], r[j + 3]), pack2(w.z, w.w), s[1]);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[b]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) { mbar_arrive(&tempty[b]); mbar_arrive(&sempty[ss]); }
+        if (lane == 0) mbar_arrive(&sempty[ss]);
       }
       if (!ok) break;
       if (split > 1) {
@@ -373,11 +409,16 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         // loads have all been consumed (one tile per CTA when split)
         float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) red[j * kRowsP + prow] = acc[j];
+        for (int j = 0; j < NT; j += 2) unpack2(acc[j >> 1], red[j * kRowsP + prow], red[(j + 1) * kRowsP + prow]);
       } else if (prow < ti.cols) {
+        TO* o = out + (size_t)ti.m0 * a.ldo + ti.n0 + prow;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j < ti.rows) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, acc[j]);
+        for (int j = 0; j < NT; j += 2) {
+          float lo, hi;
+          unpack2(acc[j >> 1], lo, hi);
+          if (j < ti.rows) store_val(o + (size_t)j * a.ldo, lo);
+          if (j + 1 < ti.rows) store_val(o + (size_t)(j + 1) * a.ldo, hi);
+        }
       }
     }
   }
@@ -385,15 +426,26 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     __syncwarp();
     pair2::cluster_sync();
     Tile ti;
-    if (warp >= 2 && first < ntiles && decode<NT, kRowsP>(a, s_tiles, s_off, first, ti)) {
-      const int prow = 32 * (warp & 3) + lane;
+    if (first < ntiles && decode<NT, kRowsP>(a, s_tiles, s_off, first, ti)) {
+      // columns [j0, j1) are this CTA's, one per warp at a time; a lane adds four
+      // rows of it over the ranks, all of whose loads are under way at once
       const int j0 = NT * (int)rank / split, j1 = min(NT * ((int)rank + 1) / split, ti.rows);
       TO* out = static_cast<TO*>(a.out);
       const float* red = reinterpret_cast<const float*>(smem);
-      for (int j = j0; j < j1; ++j) {
-        float v = 0.f;
-        for (int s = 0; s < split; ++s) v += ld_cluster(pair2::map_to_rank(red + j * kRowsP + prow, s));
-        if (prow < ti.cols) store_val(out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + prow, v);
+      for (int j = j0 + warp; j < j1; j += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < split) v[s] = ld_cluster4(pair2::map_to_rank(red + j * kRowsP + 4 * lane, s));
+        float4 x = v[0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+          if (s < split) { x.x += v[s].x; x.y += v[s].y; x.z += v[s].z; x.w += v[s].w; }
+        TO* o = out + (size_t)(ti.m0 + j) * a.ldo + ti.n0 + 4 * lane;
+        const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * lane + i < ti.cols) store_val(o + i, f[i]);
       }
     }
     __syncwarp();
@@ -827,7 +879,7 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
   const int n = tiles(nt, 128);
   int split = 1;
   if (!g.offsets)
-    while (split < 8 && 2 * split <= KB && (long)n * split * 2 <= 2L * sms) split *= 2;
+    while (split < 8 && split < KB && (long)n * (split + 1) <= 2L * sms) ++split;
   switch (nt) {
     case 16: return tall<16>(g, n, split, sms, dev, st);
     case 32: return tall<32>(g, n, split, sms, dev, st);
