@@ -253,6 +253,8 @@ void launch_gather_rows(const void* z, const int32_t* perm, void* zp, long P, in
 // box_rows boxes, 128-byte swizzle
 bool make_tmap_codes(CUtensorMap* map, const void* base, long rows, int K, long pitch,
                      int box_rows);
+// fp32 / bf16 output matrix, rows ld elements apart, 32-row x 128-byte boxes, swizzled
+bool make_tmap_out(CUtensorMap* map, void* base, long rows, int cols, long ld, moe_dtype dt);
 }  // namespace lmoe
 
 // Stand-alone operators (ops_api.cu checks the arguments)

@@ -57,7 +57,7 @@ struct Fp8Args {
   long ldo;
   int M, N, KB, G, NB;
   int split;                // CTAs per tile (cluster size), TALL only
-  int vec;                  // out rows take 16-byte stores
+  int vec;                  // out rows start on 16 bytes and are whole 16 bytes (TMA stores)
 };
 
 __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
@@ -100,6 +100,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 // cluster-scope release form costs about 1300 cycles per arrival.
 __device__ __forceinline__ void arrive_tmem(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// a staged box of 32 rows x 128 bytes to the output matrix; columns past its
+// width are not written
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
@@ -460,7 +467,7 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 // Wide form: 256 activation rows x 256 weight rows on an SM pair.
 // ---------------------------------------------------------------------------
 constexpr int kWN = 256;                       // weight rows per tile
-constexpr int kWStages = 5;
+constexpr int kWStages = 4;
 constexpr int kWWarps = 8;                     // promoting warps per CTA
 constexpr int kWCols = 128;                    // columns per promoting thread
 constexpr int kWThreads = 128 + 32 * kWWarps;
@@ -468,13 +475,13 @@ constexpr int kWThreads = 128 + 32 * kWWarps;
 // (128 x 40), which leaves the promoting two 232 (256 x 232)
 constexpr int kWRegsLow = 40, kWRegsHigh = 232;
 constexpr int kWStageBytes = 2 * kPBytes;      // 128 activation rows and 128 weight rows
-constexpr int kWOutBytes = 32 * 128;           // output staging of a promoting warp
+constexpr int kWOutBytes = 32 * 128;           // output staging: 32 rows of 128 bytes
 
 template <bool ROWS>
 struct WCfg {
   static constexpr int kScaleFloats = ROWS ? kWN : 0;       // column scales of a step
   static constexpr int kOutOffset = kWStages * kWStageBytes;
-  static constexpr int kScaleOffset = kOutOffset + kWWarps * kWOutBytes;
+  static constexpr int kScaleOffset = kOutOffset + kWWarps * 2 * kWOutBytes;
   static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
   static constexpr int kTableOffset = kBarOffset + 512;
   static constexpr int bytes(int groups) {
@@ -497,7 +504,7 @@ __device__ __forceinline__ int pair_cols(int cols) { return (cols + 31) & ~31; }
 template <bool ROWS, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                const Fp8Args a, const int n_tiles) {
+                const __grid_constant__ CUtensorMap omap, const Fp8Args a, const int n_tiles) {
   using C = WCfg<ROWS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -640,7 +647,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
     const uint32_t tempty_leader = pair2::map_to_rank(tempty, 0);
     const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
-    uint8_t* stage = smem + C::kOutOffset + (warp - 4) * kWOutBytes;
+    uint8_t* stage = smem + C::kOutOffset + (warp - 4) * 2 * kWOutBytes;
     TO* out = static_cast<TO*>(a.out);
     uint32_t it = 0;
     // scales of this thread's row (times its 128 columns' block scale) are read
@@ -721,13 +728,19 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       ok = t < ntiles && decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti);
       if (ok) open(ti);
       // out: 128 bytes of each of the warp's 32 rows at a time through shared
-      // memory (16-byte pieces, exclusive-or swizzled), so that a store
-      // instruction writes whole 128-byte runs of four rows
-      constexpr int V = 16 / sizeof(TO), W = 8 * V;        // columns per piece, per pass
+      // memory (16-byte pieces, exclusive-or swizzled as the output map says); 32
+      // whole rows leave by one TMA store, behind which the warp goes on (16-byte
+      // stores to 32 rows each held it about 6500 cycles a tile, whole-run
+      // stores 4000).  The last rows of a group are stored row by row: what lies
+      // behind them is not this group's.
+      constexpr int V = 16 / sizeof(TO), W = 8 * V;        // columns per 16 bytes, per pass
       const int rows = cur.rows - r0;
 #pragma unroll
       for (int c = 0; c < kWCols; c += W) {
         if (c0 + c >= qn) break;
+        uint8_t* buf = stage + ((c / W) & 1) * kWOutBytes;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // buf's last store
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           uint4 v;
@@ -739,29 +752,39 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             if constexpr (sizeof(TO) == 2) *reinterpret_cast<__nv_bfloat162*>(e + i) = __floats2bfloat162_rn(lo, hi);
             else { e[i] = lo; e[i + 1] = hi; }
           }
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
         }
+        const bool whole = a.vec && rows >= 32;
+        if (whole) fence_proxy_async();
         __syncwarp();
-        const int h = lane & 7, col = c0 + c + h * V;
+        if (lane == 0) {
+          if (whole) tma_store_2d(&omap, buf, cur.n0 + c0 + c, cur.m0 + r0);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        if (!whole) {
+          const int h = lane & 7, col = c0 + c + h * V;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((h ^ (r & 7)) << 4));
-          if (r < rows) {
-            TO* o = out + (size_t)(cur.m0 + r0 + r) * a.ldo + cur.n0 + col;
-            if (a.vec && col + V <= qn) {
-              *reinterpret_cast<uint4*>(o) = v;
-            } else {
-              const TO* e = reinterpret_cast<const TO*>(&v);
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + ((h ^ (r & 7)) << 4));
+            if (r < rows) {
+              TO* o = out + (size_t)(cur.m0 + r0 + r) * a.ldo + cur.n0 + col;
+              if (a.vec && col + V <= qn) {
+                *reinterpret_cast<uint4*>(o) = v;
+              } else {
+                const TO* e = reinterpret_cast<const TO*>(&v);
 #pragma unroll
-              for (int x = 0; x < V; ++x)
-                if (col + x < qn) o[x] = e[x];
+                for (int x = 0; x < V; ++x)
+                  if (col + x < qn) o[x] = e[x];
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -781,7 +804,8 @@ Fp8Args args_of(const moe_fp8_gemm& g) {
   a.offsets = g.offsets; a.out = g.out; a.ldo = g.ldo; a.M = g.M; a.N = g.N;
   a.KB = ceil_div(g.K, 128); a.G = g.offsets ? g.n_groups : 1; a.NB = ceil_div(g.N, 128);
   a.split = 1;
-  a.vec = (g.ldo * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+  // a TMA store writes whole 16 bytes at the matrix's right edge
+  a.vec = (g.ldo * es) % 16 == 0 && (g.N * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
   return a;
 }
 
@@ -840,12 +864,13 @@ cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
     pairs[dev] = n > 0 ? n : 1;
   }
   const Fp8Args a = args_of(g);
-  CUtensorMap am, bm;
+  CUtensorMap am, bm, om = {};
   if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, kRowsP) ||
-      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP))
+      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP) ||
+      (a.vec && !make_tmap_out(&om, g.out, g.M, g.N, g.ldo, g.out_dtype)))
     return cudaErrorInvalidValue;
   const int n = n_tiles < pairs[dev] ? n_tiles : pairs[dev];
-  kern<<<2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st>>>(am, bm, a, n_tiles);
+  kern<<<2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st>>>(am, bm, om, a, n_tiles);
   return cudaGetLastError();
 }
 
