@@ -72,6 +72,12 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // already taken come below every score.
 constexpr uint32_t kKeyOut = 1u, kKeyTaken = 0u;
 
+__device__ __forceinline__ float rcp_approx(float v) {     // within 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
@@ -251,7 +257,8 @@ __device__ __noinline__ void select_exact(const TopkArgs& a, long t, int lane, f
 // A row takes about 1000 warp instructions at 512 experts, and instruction issue
 // is what bounds it: 16384 x 512, k = 22, ROUTE_US us, against 92 us for fp64
 // scores of all experts and k arg-max rounds.
-template <typename TL, int EPL, bool SOFTMAX>
+// FULL: E == 32 EPL, no lane has an index past the row.
+template <typename TL, int EPL, bool SOFTMAX, bool FULL>
 __global__ void __launch_bounds__(32 * kRows, EPL <= 8 ? 5 : EPL == 16 ? 4 : 2)
 route_topk_kernel(const TopkArgs a) {
   extern __shared__ float s_dyn[];
@@ -262,14 +269,18 @@ route_topk_kernel(const TopkArgs a) {
   float* buf = s_dyn + (size_t)warp * (a.E + 64);          // n_group > 1 only
   float* sel = s_sel[warp];
   uint64_t* keys = s_key[warp];
+  auto in = [&](int i) { return FULL || lane + 32 * i < a.E; };
   float b[EPL], bmax = 0.f;
+  bool odd = false;                                        // a NaN or -inf bias
   const bool by_logit = SOFTMAX && !a.bias && a.n_group == 1;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.f;
+    b[i] = a.bias && in(i) ? a.bias[lane + 32 * i] : 0.f;
     if (b[i] > -INFINITY) bmax = fmaxf(bmax, fabsf(b[i]));   // an expert out by its bias has no say
+    else odd = true;
   }
   bmax = warp_max(bmax);
+  odd = __any_sync(kAll, odd);
 
   for (long t = (long)blockIdx.x * warps + warp; t < a.T; t += (long)gridDim.x * warps) {
     const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.ld;
@@ -277,7 +288,7 @@ route_topk_kernel(const TopkArgs a) {
     float m = -INFINITY, d;
     double sum = 1.0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = lane + 32 * i < a.E ? load_logit(row + lane + 32 * i) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) c[i] = in(i) ? load_logit(row + lane + 32 * i) : -INFINITY;
     if (SOFTMAX) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) m = fmaxf(m, c[i]);
@@ -312,15 +323,17 @@ route_topk_kernel(const TopkArgs a) {
       for (int i = 0; i < EPL; ++i) {
         const float l = c[i], x = fmaxf(l, -80.f);
         big = fmaxf(big, fabsf(x));
-        c[i] = l > -INFINITY ? __fdividef(1.f, 1.f + __expf(-x)) + b[i] : -INFINITY;
+        c[i] = l > -INFINITY ? rcp_approx(1.f + __expf(-x)) + b[i] : -INFINITY;
       }
       d = (__any_sync(kAll, big > 16.f) ? 0x1p-17f : 0x1p-19f) * (2.f + bmax) + 1e-34f;
     }
-    bool open = !(d < INFINITY) || a.k > 32;               // an infinite bias
-    if (a.n_group > 1) {
+    if (odd) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (!(c[i] > -INFINITY)) c[i] = -INFINITY;         // a NaN bias
+        if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
+    }
+    bool open = !(d < INFINITY) || a.k > 32;               // an infinite bias
+    if (a.n_group > 1) {
       float gs[2];
       group_sums<EPL>(c, a.E, a.n_group, lane, buf, gs);
       const uint64_t keep = best_groups(gs, a.n_group, a.topk_group, lane);
@@ -340,15 +353,14 @@ route_topk_kernel(const TopkArgs a) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = lane + 32 * i;
-        if (e < a.E && !(keep >> (e / G) & 1)) c[i] = -INFINITY;
+        if (in(i) && !(keep >> (e / G) & 1)) c[i] = -INFINITY;
       }
     }
     float top = -INFINITY, low = INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (!SOFTMAX || !by_logit) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;   // a NaN bias
       top = fmaxf(top, c[i]);
-      if (lane + 32 * i < a.E) low = fminf(low, c[i]);
+      if (in(i)) low = fminf(low, c[i]);
     }
     int n = a.E;                                           // eligible experts
     if (!__all_sync(kAll, low > -INFINITY)) {
@@ -363,16 +375,8 @@ route_topk_kernel(const TopkArgs a) {
       // a lane without an expert: start at the lowest finite value
       float lo = fmaxf(-warp_max(-top), -FLT_MAX), hi = warp_max(top);
       while (true) {
-        cut = lo - 2.f * d;
-        n = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) n += c[i] >= cut;
-        n = __reduce_add_sync(kAll, n);
-        if (n <= 32) {
-          open = by_logit && lo - m < -80.f;
-          break;
-        }
-        // raise lo: to the middle, or down towards it while fewer than k reach that
+        // raise lo: to the middle, or down towards it while fewer than k reach
+        // that, until at most 32 experts are left above it
         bool moved = false;
         while (true) {
           const float x = 0.5f * lo + 0.5f * hi;
@@ -385,6 +389,15 @@ route_topk_kernel(const TopkArgs a) {
           lo = x;
           moved = true;
           if (r <= 32) break;
+        }
+        cut = lo - 2.f * d;
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) n += c[i] >= cut;
+        n = __reduce_add_sync(kAll, n);
+        if (n <= 32) {
+          open = by_logit && lo - m < -80.f;
+          break;
         }
         if (!moved) { open = true; break; }
       }
@@ -546,19 +559,23 @@ route_topk_bwd_kernel(const TopkBwdArgs a) {
   }
 }
 
-template <typename TL, bool SOFTMAX>
-cudaError_t topk_launch(const TopkArgs& a, cudaStream_t st) {
+template <typename TL, int EPL, bool SOFTMAX>
+cudaError_t topk_epl(const TopkArgs& a, cudaStream_t st) {
   // few rows: one warp per CTA, so that each has an SM's issue slots to itself
   const int warps = a.T >= 2048 ? kRows : a.T >= 512 ? 4 : 1;
   const int need = ceil_div(a.T, warps), grid = need < 148 * 8 ? need : 148 * 8;
-  const int threads = 32 * warps, epl = ceil_div(a.E, 32);
   const size_t sm = a.n_group > 1 ? (size_t)warps * (a.E + 64) * 4 : 0;      // at most 34 KB
-  if (epl <= 1) route_topk_kernel<TL, 1, SOFTMAX><<<grid, threads, sm, st>>>(a);
-  else if (epl <= 4) route_topk_kernel<TL, 4, SOFTMAX><<<grid, threads, sm, st>>>(a);
-  else if (epl <= 8) route_topk_kernel<TL, 8, SOFTMAX><<<grid, threads, sm, st>>>(a);
-  else if (epl <= 16) route_topk_kernel<TL, 16, SOFTMAX><<<grid, threads, sm, st>>>(a);
-  else route_topk_kernel<TL, 32, SOFTMAX><<<grid, threads, sm, st>>>(a);
+  if (a.E == 32 * EPL) route_topk_kernel<TL, EPL, SOFTMAX, true><<<grid, 32 * warps, sm, st>>>(a);
+  else route_topk_kernel<TL, EPL, SOFTMAX, false><<<grid, 32 * warps, sm, st>>>(a);
   return cudaGetLastError();
+}
+
+template <typename TL, bool SOFTMAX>
+cudaError_t topk_launch(const TopkArgs& a, cudaStream_t st) {
+  const int epl = ceil_div(a.E, 32);
+  return epl <= 1 ? topk_epl<TL, 1, SOFTMAX>(a, st) : epl <= 4 ? topk_epl<TL, 4, SOFTMAX>(a, st)
+       : epl <= 8 ? topk_epl<TL, 8, SOFTMAX>(a, st) : epl <= 16 ? topk_epl<TL, 16, SOFTMAX>(a, st)
+                                                    : topk_epl<TL, 32, SOFTMAX>(a, st);
 }
 
 template <typename TL, bool SOFTMAX>
@@ -583,7 +600,7 @@ cudaError_t topk_bwd_launch(const TopkBwdArgs& a, cudaStream_t st) {
 // index outside [0, E) go nowhere: pos -1, and the tail of perm that they leave
 // is -1 too.
 // ---------------------------------------------------------------------------
-constexpr int kPairs = 1024;
+constexpr int kPairs = 1024, kPairWarps = kPairs / 32;
 
 struct GroupArgs {
   const int32_t* idx;
@@ -652,10 +669,10 @@ __device__ __forceinline__ int block_prefix(int v, int* s_warp) {
 // the first writes them out as offsets
 __global__ void __launch_bounds__(kPairs)
 group_place_kernel(const GroupArgs a) {
-  extern __shared__ uint8_t s_cnt[];                   // [32 warps][E] pairs of a warp
+  extern __shared__ uint16_t s_cnt[];                  // [kPairWarps][E] pairs of a warp, then before it
   __shared__ int s_base[1024], s_warp[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < 8 * a.E; i += kPairs) reinterpret_cast<uint32_t*>(s_cnt)[i] = 0u;
+  for (int i = threadIdx.x; i < kPairWarps / 2 * a.E; i += kPairs) reinterpret_cast<uint32_t*>(s_cnt)[i] = 0u;
   const int c = threadIdx.x < a.E ? a.counts[threadIdx.x] : 0;
   const int off = block_prefix(c, s_warp);             // (a barrier: s_cnt is cleared)
   if (threadIdx.x < a.E) {
@@ -670,12 +687,22 @@ group_place_kernel(const GroupArgs a) {
   if (e >= a.E) e = -1;
   const unsigned same = __match_any_sync(0xffffffffu, e);
   const int below = __popc(same & ((1u << lane) - 1u));
-  if (e >= 0 && below == 0) s_cnt[warp * a.E + e] = (uint8_t)__popc(same);
+  if (e >= 0 && below == 0) s_cnt[warp * a.E + e] = (uint16_t)__popc(same);
+  __syncthreads();
+  // a column per thread: the pairs of its expert in earlier warps
+  if (threadIdx.x < a.E) {
+    int run = 0;
+#pragma unroll 8
+    for (int i = 0; i < kPairWarps; ++i) {
+      const int v = s_cnt[i * a.E + threadIdx.x];
+      s_cnt[i * a.E + threadIdx.x] = (uint16_t)run;
+      run += v;
+    }
+  }
   __syncthreads();
   if (p >= a.P) return;
   if (e < 0) { a.pos[p] = -1; return; }
-  int q = s_base[e] + below;
-  for (int i = 0; i < warp; ++i) q += s_cnt[i * a.E + e];
+  const int q = s_base[e] + s_cnt[warp * a.E + e] + below;
   a.pos[p] = q;
   a.perm[q] = (int32_t)p;
 }
@@ -714,7 +741,13 @@ cudaError_t launch_route_group(const int32_t* idx, long P, int E, int32_t* count
                     static_cast<int32_t*>(ws)};
   group_count_kernel<<<a.nblk, kPairs, (size_t)E * 4, st>>>(a);
   group_scan_kernel<<<ceil_div(E, 8), 256, 0, st>>>(a);
-  group_place_kernel<<<a.nblk, kPairs, (size_t)E * 32, st>>>(a);
+  const size_t sm = (size_t)E * kPairWarps * 2;               // at most 64 KB
+  if (sm > 48 * 1024 - 4500) {
+    const cudaError_t e = cudaFuncSetAttribute(group_place_kernel,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  group_place_kernel<<<a.nblk, kPairs, sm, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -222,35 +222,34 @@ def _gate_kind(gate, T, D):
     return B.MOE_GATE_TOKEN
 
 
-def _norm_args(T, D, dt, x, y, r, post_weight, gate, residual_scale, pre_weight, eps):
-    """The fields that forward and backward share; the tensors whose pointers
-    they hold are kept in the second result."""
-    a = B.moe_norm_args(T, D, dt, _gate_kind(gate, T, D), residual_scale, eps)
+def _norm_inputs(T, D, r, y, post_weight, gate, pre_weight):
+    """(kind, y, ldy, post_weight, pre_weight, gate, ldg) as the library reads
+    them: checked against r's shape, type and device, copied where unaligned."""
     dev, dtype = r.get_device(), r.dtype
     if y.shape != r.shape or y.dtype != dtype or y.get_device() != dev:
         _bad("y must have x's shape, type and device")
-    y, a.ldy = _rows16(y)
-    a.y = y.data_ptr()
+    y, ldy = _rows16(y)
     if post_weight is not None:
         _like(post_weight, "post_weight", dev, dtype, (D,))
         post_weight = _vec16(post_weight)
-        a.post_weight = post_weight.data_ptr()
     if pre_weight is not None:
         _like(pre_weight, "pre_weight", dev, dtype, (D,))
         pre_weight = _vec16(pre_weight)
-        a.pre_weight = pre_weight.data_ptr()
-    if gate is not None:
+    kind, ldg = _gate_kind(gate, T, D), 0
+    if kind:
         if gate.dtype != dtype or gate.get_device() != dev:
             _bad("gate must have x's type and device")
-        if a.gate_kind == B.MOE_GATE_FULL:
-            gate, a.ldg = _rows16(gate)
-        elif a.gate_kind == B.MOE_GATE_TOKEN:
-            gate = gate.contiguous()
-            a.ldg = 1
+        if kind == B.MOE_GATE_FULL:
+            gate, ldg = _rows16(gate)
+        elif kind == B.MOE_GATE_TOKEN:
+            gate, ldg = gate.contiguous(), 1
         else:
             gate = _vec16(gate)
-        a.gate = gate.data_ptr()
-    return a, (y, post_weight, pre_weight, gate)
+    return kind, y, ldy, post_weight, pre_weight, gate, ldg
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def norm_residual(x, y, *, post_weight=None, gate=None, residual_scale=1.0, pre_weight=None,
@@ -267,23 +266,15 @@ def norm_residual(x, y, *, post_weight=None, gate=None, residual_scale=1.0, pre_
                                  stats=stats)
     T, D = x.shape
     where, dtype = x.device, x.dtype
-    a, keep = _norm_args(T, D, dt, x, y, x, post_weight, gate, residual_scale, pre_weight, eps)
-    x, a.ldx = _rows16(x)
-    a.x = x.data_ptr()
+    kind, y, ldy, post, pre, gate, ldg = _norm_inputs(T, D, x, y, post_weight, gate, pre_weight)
+    x, ldx = _rows16(x)
     r = _empty(T, D, dtype=dtype, device=where)
-    a.r, a.ldr = r.data_ptr(), D
-    h = ry = rr = None
-    if pre_weight is not None:
-        h = _empty(T, D, dtype=dtype, device=where)
-        a.h, a.ldh = h.data_ptr(), D
-    if stats:
-        if post_weight is not None:
-            ry = _empty(T, dtype=_F32, device=where)
-            a.rstd_y = ry.data_ptr()
-        if pre_weight is not None:
-            rr = _empty(T, dtype=_F32, device=where)
-            a.rstd_r = rr.data_ptr()
-    B.moe_norm_residual(a, _stream(dev))
+    h = None if pre is None else _empty(T, D, dtype=dtype, device=where)
+    ry = _empty(T, dtype=_F32, device=where) if stats and post is not None else None
+    rr = _empty(T, dtype=_F32, device=where) if stats and pre is not None else None
+    B.moe_norm_residual(B.moe_norm_args(
+        T, D, dt, kind, residual_scale, eps, x.data_ptr(), ldx, y.data_ptr(), ldy, _at(post),
+        _at(pre), _at(gate), ldg, r.data_ptr(), D, _at(h), D, _at(ry), _at(rr)), _stream(dev))
     return NormForward(r, h, ry, rr)
 
 
@@ -293,12 +284,11 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
     from dr (None for zero) and dh (with pre_weight): dx, dy in their type,
     dpost_weight, dpre_weight fp32 [D], dgate fp32 [D] / [T, 1] or [T, D] in the
     gate's type."""
-    r = forward.r
+    r, _, ry, rr = forward
     dev, dt = _input(r, "forward.r")
     if (dh is not None) != (pre_weight is not None):
         _bad("dh goes with pre_weight")
-    if post_weight is not None and forward.rstd_y is None or \
-            pre_weight is not None and forward.rstd_r is None:
+    if post_weight is not None and ry is None or pre_weight is not None and rr is None:
         _bad("forward ran without stats")
     if dev != _device():
         with _on(dev):
@@ -306,37 +296,40 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
                                           residual_scale=residual_scale, pre_weight=pre_weight)
     T, D = r.shape
     where, dtype = r.device, r.dtype
-    a, keep = _norm_args(T, D, dt, None, y, r, post_weight, gate, residual_scale, pre_weight, 1.0)
-    r, a.ldr = _rows16(r)
-    a.r = r.data_ptr()
+    shape = None if gate is None else gate.shape
+    kind, y, ldy, post, pre, gate, ldg = _norm_inputs(T, D, r, y, post_weight, gate, pre_weight)
+    r, ldr = _rows16(r)
+    lddr = lddh = 0
     if dr is not None:
         _like(dr, "dr", dev, dtype, (T, D))
-        dr, a.lddr = _rows16(dr)
-        a.dr = dr.data_ptr()
+        dr, lddr = _rows16(dr)
+    if dh is not None:
+        _like(dh, "dh", dev, dtype, (T, D))
+        dh, lddh = _rows16(dh)
+    if post is not None:
+        _like(ry, "forward.rstd_y", dev, _F32, (T,))
+    if pre is not None:
+        _like(rr, "forward.rstd_r", dev, _F32, (T,))
     dx = _empty(T, D, dtype=dtype, device=where)
     dy = _empty(T, D, dtype=dtype, device=where)
-    a.dx, a.lddx, a.dy, a.lddy = dx.data_ptr(), D, dy.data_ptr(), D
-    dpost = dpre = dgate = None
-    if post_weight is not None:
-        _like(forward.rstd_y, "forward.rstd_y", dev, _F32, (T,))
-        a.rstd_y = forward.rstd_y.data_ptr()
-        dpost = _empty(D, dtype=_F32, device=where)
-        a.dpost_weight = dpost.data_ptr()
-    if pre_weight is not None:
-        _like(dh, "dh", dev, dtype, (T, D))
-        _like(forward.rstd_r, "forward.rstd_r", dev, _F32, (T,))
-        dh, a.lddh = _rows16(dh)
-        a.dh = dh.data_ptr()
-        a.rstd_r = forward.rstd_r.data_ptr()
-        dpre = _empty(D, dtype=_F32, device=where)
-        a.dpre_weight = dpre.data_ptr()
-    if gate is not None:
-        dgate = _empty(*gate.shape, dtype=dtype if a.gate_kind == B.MOE_GATE_FULL else _F32,
-                       device=where)
-        a.dgate, a.lddg = dgate.data_ptr(), D
-    n = B.moe_norm_residual_workspace(T, D)
-    ws = _empty(n, dtype=_U8, device=where)
-    B.moe_norm_residual_backward(a, ws.data_ptr(), n, _stream(dev))
+    # the workspace and the column sums in one buffer
+    need = B.moe_norm_residual_workspace(T, D)
+    ws = (need + 15) // 16 * 4
+    buf = _empty(ws + 3 * D, dtype=_F32, device=where)
+    at, v = buf.data_ptr(), buf.as_strided
+    dpost = None if post is None else v((D,), (1,), ws)
+    dpre = None if pre is None else v((D,), (1,), ws + D)
+    dgate = at_gate = None
+    if kind == B.MOE_GATE_CHANNEL:
+        dgate, at_gate = v((D,), (1,), ws + 2 * D), at + 4 * (ws + 2 * D)
+    elif kind:
+        dgate = _empty(*shape, dtype=dtype if kind == B.MOE_GATE_FULL else _F32, device=where)
+        at_gate = dgate.data_ptr()
+    B.moe_norm_residual_backward(B.moe_norm_args(
+        T, D, dt, kind, residual_scale, 1.0, None, 0, y.data_ptr(), ldy, _at(post), _at(pre),
+        _at(gate), ldg, r.data_ptr(), ldr, None, 0, _at(ry), _at(rr), _at(dr), lddr, _at(dh), lddh,
+        dx.data_ptr(), D, dy.data_ptr(), D, None if post is None else at + 4 * ws,
+        None if pre is None else at + 4 * (ws + D), at_gate, D), at, need, _stream(dev))
     return NormBackward(dx, dy, dpost, dpre, dgate)
 
 
