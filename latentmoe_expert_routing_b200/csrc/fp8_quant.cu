@@ -164,8 +164,13 @@ quant_rows_kernel(const QuantArgs a) {
     const T* row = static_cast<const T*>(a.x) + (ok ? src : 0) * a.ldx;
     Raw8<T> v[kQBlocks];
     float m[kQBlocks];
+    if (a.vec && (kb0 + kQBlocks) * 128 <= a.K && ok) {
 #pragma unroll
-    for (int b = 0; b < kQBlocks; ++b) load_row8(row, (kb0 + b) * 128 + sub * 8, ok ? a.K : 0, a.vec, v[b]);
+      for (int b = 0; b < kQBlocks; ++b) v[b].load(row + (kb0 + b) * 128 + sub * 8);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kQBlocks; ++b) load_row8(row, (kb0 + b) * 128 + sub * 8, ok ? a.K : 0, a.vec, v[b]);
+    }
 #pragma unroll
     for (int b = 0; b < kQBlocks; ++b) m[b] = v[b].template amax<RELU2>();
 #pragma unroll
@@ -289,8 +294,13 @@ quant_square_kernel(const QuantArgs a) {
   const int r0 = nb * 128 + 8 * rl, c0 = kb * 128 + 8 * sub;
   Raw8<T> v[8];
   float m = 0.f;
+  if (a.vec && (nb + 1) * 128 <= a.rows && (kb + 1) * 128 <= a.K) {    // no branch between the loads
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_row8(x + (long)(r0 + i) * a.ldx, c0, r0 + i < a.rows ? a.K : 0, a.vec, v[i]);
+    for (int i = 0; i < 8; ++i) v[i].load(x + (long)(r0 + i) * a.ldx + c0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_row8(x + (long)(r0 + i) * a.ldx, c0, r0 + i < a.rows ? a.K : 0, a.vec, v[i]);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i].template amax<false>());
 #pragma unroll

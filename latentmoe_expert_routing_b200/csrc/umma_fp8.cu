@@ -44,7 +44,6 @@ __device__ int g_fp8_err;
 constexpr int kRowsP = 128;               // MMA rows of a tile
 constexpr int kKB = 128;                  // K elements (bytes) per step
 constexpr int kPBytes = kRowsP * kKB;
-constexpr int kScaleRing = 8;
 constexpr int kMaxGroups = 1024;
 
 struct Fp8Args {
@@ -72,16 +71,6 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t ad, uint64_t bd, 
 // fp32 accumulator, E4M3 operands (format 0), both K-major
 __device__ __forceinline__ uint32_t idesc_f8(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// 4 bytes to shared memory, zeros when !ok
-__device__ __forceinline__ void cp_async4(float* dst, const float* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0) : "memory");
-}
-// the barrier gets this thread's arrival once its cp.async so far have landed
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -477,12 +466,14 @@ constexpr int kWRegsLow = 40, kWRegsHigh = 232;
 constexpr int kWStageBytes = 2 * kPBytes;      // 128 activation rows and 128 weight rows
 constexpr int kWOutBytes = 32 * 128;           // output staging: 32 rows of 128 bytes
 
+constexpr int kWScaleSteps = 2, kWScaleSlots = 4;    // column scales: steps per slot, slots
+
 template <bool ROWS>
 struct WCfg {
-  static constexpr int kScaleFloats = ROWS ? kWN : 0;       // column scales of a step
+  static constexpr int kScaleFloats = ROWS ? kWScaleSteps * kWN : 0;   // column scales of a slot
   static constexpr int kOutOffset = kWStages * kWStageBytes;
   static constexpr int kScaleOffset = kOutOffset + kWWarps * 2 * kWOutBytes;
-  static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleFloats * 4;
+  static constexpr int kBarOffset = kScaleOffset + kWScaleSlots * kScaleFloats * 4;
   static constexpr int kTableOffset = kBarOffset + 512;
   static constexpr int bytes(int groups) {
     return kTableOffset + (groups ? 2 * (groups + 1) * 4 : 0) + 1024;
@@ -514,8 +505,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
   uint64_t* done = full + kWStages;                                      // a step's products are
                                                                          // finished: both CTAs
   uint64_t* sfull = done + kWStages;                                     // own scales
-  uint64_t* sempty = sfull + kScaleRing;
-  uint64_t* tempty = sempty + kScaleRing;                                // [2] the leader's are used
+  uint64_t* sempty = sfull + kWScaleSlots;
+  uint64_t* tempty = sempty + kWScaleSlots;                              // [2] the leader's are used
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -528,7 +519,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWStages; ++s) { mbar_init(&full[s], 1); mbar_init(&done[s], 1); }
-    for (int s = 0; s < kScaleRing; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], kWWarps); }
+    for (int s = 0; s < kWScaleSlots; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], kWWarps); }
     for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * kWWarps);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -590,25 +581,45 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ---------------- column scales by cp.async (both CTAs) ----------------
+      // ---------------- column scales, kWScaleSteps steps at a time (both CTAs) ----------------
       if constexpr (ROWS) {
-        uint32_t it = 0;
+        uint32_t sl = 0;
         bool ok = true;
+        // whole 16 bytes where the rows of scales allow it
+        const bool vec = a.ldsb % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sb) & 15u) == 0;
         for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
           Tile ti;
           if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
           const float* sb = a.sb + ti.n0;
-          for (int kb = 0; kb < a.KB; ++kb, ++it, sb += a.ldsb) {
-            const uint32_t ss = it % kScaleRing;
-            ok = mbar_wait(&sempty[ss], ((it / kScaleRing) & 1) ^ 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
-            float* sc = s_scale + ss * C::kScaleFloats;
+          for (int kb = 0; kb < a.KB; kb += kWScaleSteps, ++sl) {
+            const uint32_t ss = sl % kWScaleSlots;
+            float4 v[kWScaleSteps][2];
 #pragma unroll
-            for (int i = lane; i < kWN; i += 32) cp_async4(sc + i, sb + (i < ti.cols ? i : 0), i < ti.cols);
-            cp_async_arrive(&sfull[ss]);
+            for (int k = 0; k < kWScaleSteps; ++k, sb += a.ldsb)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int i = 4 * lane + 128 * h;
+                v[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (kb + k >= a.KB) continue;
+                if (vec && i + 4 <= ti.cols) {
+                  v[k][h] = __ldg(reinterpret_cast<const float4*>(sb + i));
+                } else {
+                  if (i < ti.cols) v[k][h].x = __ldg(sb + i);
+                  if (i + 1 < ti.cols) v[k][h].y = __ldg(sb + i + 1);
+                  if (i + 2 < ti.cols) v[k][h].z = __ldg(sb + i + 2);
+                  if (i + 3 < ti.cols) v[k][h].w = __ldg(sb + i + 3);
+                }
+              }
+            ok = mbar_wait(&sempty[ss], ((sl / kWScaleSlots) & 1) ^ 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+            float* sc = s_scale + ss * C::kScaleFloats + 4 * lane;
+#pragma unroll
+            for (int k = 0; k < kWScaleSteps; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) *reinterpret_cast<float4*>(sc + k * kWN + 128 * h) = v[k][h];
+            mbar_arrive(&sfull[ss]);
           }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
       }
     } else if (leader && lane == 0) {
       // ---------------- MMA issuers: warp 1 the even steps, warp 3 the odd ones ----------------
@@ -649,7 +660,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
     uint8_t* stage = smem + C::kOutOffset + (warp - 4) * 2 * kWOutBytes;
     TO* out = static_cast<TO*>(a.out);
-    uint32_t it = 0;
+    uint32_t it = 0, sl = 0;                               // steps; slots of column scales
     // scales of this thread's row (times its 128 columns' block scale) are read
     // three steps ahead; those of the next tile's first steps before this tile
     // is written out
@@ -677,7 +688,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 #pragma unroll
       for (int j = 0; j < kWCols / 2; ++j) acc[j] = 0;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
-        const uint32_t ss = it % kScaleRing, b = it & 1;
+        const uint32_t ss = sl % kWScaleSlots, b = it & 1;
+        const int within = kb % kWScaleSteps;
         const float rs = sa[0] * sb[0];
         sa[0] = sa[1]; sa[1] = sa[2]; sb[0] = sb[1]; sb[1] = sb[2];
         if (kb + 3 < a.KB) {
@@ -685,7 +697,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           pa += a.ldsa;
           if (!ROWS) sb[2] = __ldg(pb++);
         }
-        if ((ROWS && !mbar_wait(&sfull[ss], (it / kScaleRing) & 1)) ||
+        if ((ROWS && within == 0 && !mbar_wait(&sfull[ss], (sl / kWScaleSlots) & 1)) ||
             !mbar_wait(&done[it % kWStages], (it / kWStages) & 1)) {
           ok = false;
           fail();
@@ -693,7 +705,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         }
         tc_fence_after();
         const uint64_t rs2 = both(rs);
-        const float* cs = s_scale + ss * C::kScaleFloats + c0;
+        const float* cs = s_scale + ss * C::kScaleFloats + within * kWN + c0;
 #pragma unroll
         for (int c = 0; c < kWCols; c += 64) {
           if (c0 + c >= qn) break;                         // uniform in the warp
@@ -719,8 +731,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         __syncwarp();
         if (lane == 0) {
           arrive_tmem(tempty_leader + b * (uint32_t)sizeof(uint64_t));
-          if (ROWS) mbar_arrive(&sempty[ss]);
+          if (ROWS && (within == kWScaleSteps - 1 || kb == a.KB - 1)) mbar_arrive(&sempty[ss]);
         }
+        if (ROWS && (within == kWScaleSteps - 1 || kb == a.KB - 1)) ++sl;
       }
       if (!ok) break;
       const Tile cur = ti;
