@@ -822,14 +822,26 @@ Fp8Args args_of(const moe_fp8_gemm& g) {
   return a;
 }
 
+// setmaxnreg.inc takes its registers from those that the launch gave the block:
+// a kernel compiled to fewer than its split counts on would wait for ever, so it
+// is not launched
+template <typename K>
+cudaError_t check_registers(K kern, int threads, int need) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+  if (e != cudaSuccess) return e;
+  return at.numRegs * threads >= need ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 template <int NT, typename TO>
 cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
   using C = TCfg<NT>;
   auto kern = fp8_tall_kernel<NT, TO>;
   static bool configured[kMaxDevices] = {};
   if (!configured[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               C::bytes(kMaxGroups));
+    cudaError_t e = check_registers(kern, C::kThreads, 128 * kTRegsLow + 128 * kTRegsHigh);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(kMaxGroups));
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
@@ -865,8 +877,9 @@ cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
   auto kern = fp8_pair_kernel<ROWS, TO>;
   static int pairs[kMaxDevices] = {};            // co-resident pairs (0: not asked yet)
   if (!pairs[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::bytes(kMaxGroups));
+    cudaError_t e = check_registers(kern, kWThreads, 128 * kWRegsLow + 256 * kWRegsHigh);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(kMaxGroups));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sms / 2));

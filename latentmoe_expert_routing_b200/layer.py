@@ -131,6 +131,21 @@ class LatentMoE:
                             out.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), self.stream)
         return out, topk_idx, topk_w
 
+    def block_step(self, h, x, *, post_weight=None, gate=None, residual_scale=1.0,
+                   next_weight=None, eps=1e-5):
+        """One block of a residual stream whose norms lie between the blocks: the
+        layer on its normalised input h, then the stream x with the layer's output
+        normed (post_weight), gated, and added, and the next block's normalised
+        input (next_weight) -- (r, next_h or None, topk_idx, topk_w), r and next_h
+        from one norm_residual call.  Needs a layer whose out_dtype is its dtype."""
+        from .ops import norm_residual
+        if self.out_dtype != self.dtype:
+            raise ValueError("block_step needs a layer with out_dtype == dtype")
+        out, idx, w = self(h)
+        f = norm_residual(x, out, post_weight=post_weight, gate=gate,
+                          residual_scale=residual_scale, pre_weight=next_weight, eps=eps)
+        return f.r, f.h, idx, w
+
     def forward_host(self, x_host, out_host, topk_idx_host=None, topk_w_host=None):
         """Host buffers in and out (pinned is fastest); synchronises."""
         B.moe_forward_host(self.handle, x_host.data_ptr(), x_host.shape[0],
