@@ -9,6 +9,9 @@
 // weights   blocks of 128 x 128, codes as they lie and, on demand, transposed
 // All three read their input once; they are bound by memory.  The factor of a
 // block is one division, an element costs one product and half a conversion.
+// bf16: rows of 8192 x 8192 32 us (6.4 TB/s), with squared ReLU 45056 x 5120
+// 105 us (6.6 TB/s); transposed 4096 x 8192 and 4096 x 2048 together 30 us (4.2
+// TB/s); 2048 x 8192 weights both ways 20 us (3.4 TB/s).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -230,7 +230,8 @@ norm_fwd_kernel(const moe_norm_args a) {
 // dpost = g S, S = sum_t d y ry.
 //
 // Six rows of D move per row; an element costs about 17 instructions in packed
-// fp32 pairs (30 unpacked, which bounded the kernel).  T = D = 8192 bf16: NORM_BWD.
+// fp32 pairs (30 unpacked, which bounded the kernel).  T = D = 8192 bf16: 152 us
+// (5.3 TB/s), the 64 partial rows' sum 5 us more.
 template <typename T, int VPT, bool FULL, bool RING>
 __global__ void __launch_bounds__(512)
 norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {

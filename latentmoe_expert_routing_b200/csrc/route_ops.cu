@@ -255,7 +255,7 @@ __device__ __noinline__ void select_exact(const TopkArgs& a, long t, int lane, f
 // they are normal, which holds for l - m > -80 (a sum of at most 1024).
 //
 // A row takes about 1000 warp instructions at 512 experts, and instruction issue
-// is what bounds it: 16384 x 512, k = 22, ROUTE_US us, against 92 us for fp64
+// is what bounds it: 16384 x 512, k = 22, 29 us, against 92 us for fp64
 // scores of all experts and k arg-max rounds.
 // FULL: E == 32 EPL, no lane has an index past the row.
 template <typename TL, int EPL, bool SOFTMAX, bool FULL>

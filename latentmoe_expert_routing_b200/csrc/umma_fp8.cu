@@ -5,27 +5,33 @@
 // Rows of a may be grouped, group g taking weight matrix g.
 //
 // The inner sum of 128 products is one tcgen05 accumulation (kind::f8f6f4, four
-// K = 32 MMAs) into one of two TMEM buffers.  The tensor core cannot apply an
-// fp32 scale, so "promoting" warps read every 128-K partial back and add
-// scale * partial to fp32 registers while the tensor core fills the other
-// buffer.  Per 128-K step of a 128 x 256 tile the MMAs take 512 cycles and the
-// 32768 FMAs of the promotion 256, so the promotion hides behind the products.
+// K = 32 MMAs) into one of a ring of TMEM buffers.  The tensor core cannot apply
+// an fp32 scale, so "promoting" warps read every 128-K partial back and add
+// scale * partial to fp32 registers (packed pairs) while the tensor core fills
+// the other buffers.  Per 128-K step of a pair's 256 x 256 tile the MMAs take 512
+// cycles and each SM's 32768 FMAs 256, so the promotion hides behind the products.
 //
 // Two forms of the tile:
-//   wide  MMA rows = 128 activation rows, MMA columns = 256 weight rows; a
-//         thread owns one activation row, and its scale product is one number
-//         for each 128 columns (per column in the weight gradient).
-//   tall  MMA rows = 128 weight rows, MMA columns = 16..128 activation rows:
-//         for few rows, where streaming the weights is the work.  Two CTAs per
-//         SM keep more loads in flight; when the tiles cannot fill the GPU, K
-//         is split over the CTAs of a cluster, which add their sums in rank
-//         order through distributed shared memory (no atomics: one order).
+//   wide  an SM pair's 256 activation rows x 256 weight rows; a thread owns one
+//         activation row, and its scale product is one number for each 128
+//         columns (per column in the weight gradient).  8192 x 10240 x 8192:
+//         650 us, 2.1 PFLOP/s; the clock falls under this load (power), and the
+//         promotion's TMEM reads and FMAs share it with the products.
+//   tall  MMA rows = 128 weight rows, MMA columns = 16..64 activation rows: for
+//         few rows, where streaming the weights is the work.  Two CTAs per SM
+//         keep more loads in flight; when the tiles cannot fill the GPU, K is
+//         split over the CTAs of a cluster, which add their sums in rank order
+//         through distributed shared memory (no atomics: one order).
+//         64 x 10240 x 8192 with cold weights: 24.6 us, 3.4 TB/s.
 //
-// Roles: one producer warp (TMA tiles by lane 0; the scales by cp.async from
-// all lanes, in a ring of their own because the promotion reads them after the
-// tile's stage is free again), one MMA thread, 4 or 16 promoting warps.  Every
-// wait is bounded; one that runs out sets DEV_ERR_TIMEOUT and unwinds.
+// Roles: a producer thread (TMA tiles), a warp that lays scale products into a
+// ring of their own (the promotion reads them after the tile's stage is free
+// again; the wide form's row scales are read by the promoting threads), two MMA
+// threads, 4 or 8 promoting warps.  Every wait is bounded; one that runs out sets
+// DEV_ERR_TIMEOUT, and its whole warp unwinds.
 #include <cuda.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -111,12 +117,20 @@ template <int NT>
 struct TCfg {
   static constexpr int kQBytes = NT * kKB;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
-  static constexpr int kBufs = NT <= 64 ? 4 : 2;                // partial sums in TMEM
-  static constexpr int kSlots = 3;
-  static constexpr int kThreads = 256;
+  static constexpr int kStages = NT <= 32 ? 5 : 4;              // two CTAs share an SM: its shared
+  static constexpr int kBufs = 4;                               // memory, and its 512 TMEM columns,
+  static constexpr int kSlots = 3;                              // for the partial sums
+  static constexpr int kWarps = NT == 64 ? 8 : 4;               // promoting warps
+  static constexpr int kCols = NT * 4 / kWarps;                 // columns per promoting thread
+  static constexpr int kChunk = NT == 32 ? 32 : 16;             // ... read at a time (80 registers
+                                                                // a thread with 12 warps)
+  static constexpr int kThreads = 128 + 32 * kWarps;
   static constexpr int kStepFloats = NT;                        // the columns' scale products
-  static constexpr uint32_t kTmemCols = kBufs * NT;             // two CTAs share an SM's 512
+  static constexpr uint32_t kTmemCols = kBufs * NT;
+  // The promotion waits on a stage's `done`, which completes again when the stage
+  // is used again: the MMAs must not get that far ahead of it, and what holds
+  // them back is the number of buffers.
+  static_assert(kBufs <= kStages, "a done phase could pass unseen");
   static constexpr int kScaleOffset = kStages * kStageBytes;
   static constexpr int kBarOffset = kScaleOffset + kSlots * kScaleSteps * kStepFloats * 4;
   static constexpr int kTableOffset = kBarOffset + 512;
@@ -124,9 +138,16 @@ struct TCfg {
     return kTableOffset + (groups ? 2 * (groups + 1) * 4 : 0) + 1024;
   }
 };
-// registers: the launch gives 256 x 128; the first warpgroup keeps 40 a thread, which
-// leaves the promoting one 216
-constexpr int kTRegsLow = 40, kTRegsHigh = 216;
+
+// A wait of a whole warp: every lane gets the same answer, so that a wait that ran
+// out is left by all of them (the tcgen05 loads that follow need the whole warp).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool warp_aborted(const volatile int* flag) {
+  return __any_sync(0xffffffffu, *flag != 0);
+}
 
 struct Tile {
   int grp;
@@ -232,8 +253,8 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&done[s], 1); }
-    for (int s = 0; s < C::kSlots; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], 4); }
-    for (int b = 0; b < C::kBufs; ++b) mbar_init(&tempty[b], 4);
+    for (int s = 0; s < C::kSlots; ++s) { mbar_init(&sfull[s], 32); mbar_init(&sempty[s], C::kWarps); }
+    for (int b = 0; b < C::kBufs; ++b) mbar_init(&tempty[b], C::kWarps);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -256,7 +277,6 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsLow));
     if (warp == 0) {
       // ---------------- tiles by TMA ----------------
       if (lane == 0) {
@@ -292,7 +312,7 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       // ---------------- scale products, kScaleSteps steps at a time ----------------
       uint32_t sl = 0;
       bool ok = true;
-      for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+      for (int t = first; t < ntiles && ok && !warp_aborted(abort_flag); t += step) {
         Tile ti;
         if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
         const float* sb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128) * a.KB;
@@ -309,8 +329,8 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
             for (int i = 0; i < PL; ++i)
               v[k][i] = in && lane + 32 * i < ti.rows ? __ldg(sa + lane + 32 * i) * bs : 0.f;
           }
-          ok = mbar_wait(&sempty[ss], ((sl / C::kSlots) & 1) ^ 1);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+          ok = warp_wait(&sempty[ss], ((sl / C::kSlots) & 1) ^ 1);
+          if (!ok) { fail(); break; }
           float* sc = s_scale + ss * kScaleSteps * C::kStepFloats;
 #pragma unroll
           for (int k = 0; k < kScaleSteps; ++k)
@@ -349,45 +369,38 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsHigh));
     // ---------------- promotion and store ----------------
     const int q = warp & 3;                                // TMEM lane quarter
-    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
+    const int c0 = ((warp - 4) >> 2) * C::kCols;           // first column
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
     const int prow = 32 * q + lane;                        // this thread's weight row
-    constexpr int kChunk = NT < 64 ? NT : 64;
     uint32_t it = 0, sl = 0;
     bool ok = true;
     TO* out = static_cast<TO*>(a.out);
-    for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+    for (int t = first; t < ntiles && ok && !warp_aborted(abort_flag); t += step) {
       Tile ti;
       if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
-      uint64_t acc[NT / 2];
+      uint64_t acc[C::kCols / 2];
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
+      for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
       for (int kb = kb0; kb < kb1 && ok; kb += kScaleSteps, ++sl) {
         const uint32_t ss = sl % C::kSlots;
-        if (!mbar_wait(&sfull[ss], (sl / C::kSlots) & 1)) { ok = false; fail(); break; }
+        if (!warp_wait(&sfull[ss], (sl / C::kSlots) & 1)) { ok = false; fail(); break; }
         const float* sc = s_scale + ss * kScaleSteps * C::kStepFloats;
         const int steps = min(kScaleSteps, kb1 - kb);
         for (int k = 0; k < steps; ++k, ++it, sc += C::kStepFloats) {
           const uint32_t st = it % C::kStages, b = it % C::kBufs;
-          if (!mbar_wait(&done[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
+          if (!warp_wait(&done[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < NT; c += kChunk) {
-            if (c >= ti.rows) break;                       // uniform in the warp
-            uint32_t r[kChunk];
-            if constexpr (kChunk == 16) {
-              tmem_ld16(tbase + b * NT + c, r);
-            } else {
-#pragma unroll
-              for (int h = 0; h < kChunk; h += 32)
-                pair2::tmem_ld32(tbase + b * NT + c + h, *reinterpret_cast<uint32_t(*)[32]>(r + h));
-            }
+          for (int c = 0; c < C::kCols; c += C::kChunk) {
+            uint32_t r[C::kChunk];
+            if constexpr (C::kChunk == 16) tmem_ld16(tbase + b * NT + c, r);
+            else pair2::tmem_ld32(tbase + b * NT + c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < kChunk; j += 4) {
-              const uint4 w = *reinterpret_cast<const uint4*>(sc + c + j);
+            for (int j = 0; j < C::kChunk; j += 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(sc + c0 + c + j);
               uint64_t* s = &acc[(c + j) >> 1];
               s[0] = fma2(pack2(r[j], r[j + 1]), pack2(w.x, w.y), s[0]);
               s[1] = fma2(pack2(r[j + 2], r[j + 3]), pack2(w.z, w.w), s[1]);
@@ -403,17 +416,18 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       if (split > 1) {
         // this CTA's sums for the cluster: [column][row] over the stages, whose
         // loads have all been consumed (one tile per CTA when split)
-        float* red = reinterpret_cast<float*>(smem);
+        float* red = reinterpret_cast<float*>(smem) + c0 * kRowsP + prow;
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) unpack2(acc[j >> 1], red[j * kRowsP + prow], red[(j + 1) * kRowsP + prow]);
+        for (int j = 0; j < C::kCols; j += 2) unpack2(acc[j >> 1], red[j * kRowsP], red[(j + 1) * kRowsP]);
       } else if (prow < ti.cols) {
-        TO* o = out + (size_t)ti.m0 * a.ldo + ti.n0 + prow;
+        TO* o = out + (size_t)(ti.m0 + c0) * a.ldo + ti.n0 + prow;
+        const int rows = ti.rows - c0;
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
+        for (int j = 0; j < C::kCols; j += 2) {
           float lo, hi;
           unpack2(acc[j >> 1], lo, hi);
-          if (j < ti.rows) store_val(o + (size_t)j * a.ldo, lo);
-          if (j + 1 < ti.rows) store_val(o + (size_t)(j + 1) * a.ldo, hi);
+          if (j < rows) store_val(o + (size_t)j * a.ldo, lo);
+          if (j + 1 < rows) store_val(o + (size_t)(j + 1) * a.ldo, hi);
         }
       }
     }
@@ -428,7 +442,7 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       const int j0 = NT * (int)rank / split, j1 = min(NT * ((int)rank + 1) / split, ti.rows);
       TO* out = static_cast<TO*>(a.out);
       const float* red = reinterpret_cast<const float*>(smem);
-      for (int j = j0 + warp; j < j1; j += 8) {
+      for (int j = j0 + warp; j < j1; j += C::kThreads / 32) {
         float4 v[8];
 #pragma unroll
         for (int s = 0; s < 8; ++s)
@@ -464,6 +478,7 @@ constexpr int kWThreads = 128 + 32 * kWWarps;
 // (128 x 40), which leaves the promoting two 232 (256 x 232)
 constexpr int kWRegsLow = 40, kWRegsHigh = 232;
 constexpr int kWStageBytes = 2 * kPBytes;      // 128 activation rows and 128 weight rows
+static_assert(2 <= kWStages, "two TMEM buffers: a done phase could pass unseen");
 constexpr int kWOutBytes = 32 * 128;           // output staging: 32 rows of 128 bytes
 
 constexpr int kWScaleSteps = 2, kWScaleSlots = 4;    // column scales: steps per slot, slots
@@ -587,7 +602,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         bool ok = true;
         // whole 16 bytes where the rows of scales allow it
         const bool vec = a.ldsb % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sb) & 15u) == 0;
-        for (int t = first; t < ntiles && ok && !*abort_flag; t += step) {
+        for (int t = first; t < ntiles && ok && !warp_aborted(abort_flag); t += step) {
           Tile ti;
           if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
           const float* sb = a.sb + ti.n0;
@@ -610,8 +625,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
                   if (i + 3 < ti.cols) v[k][h].w = __ldg(sb + i + 3);
                 }
               }
-            ok = mbar_wait(&sempty[ss], ((sl / kWScaleSlots) & 1) ^ 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }
+            ok = warp_wait(&sempty[ss], ((sl / kWScaleSlots) & 1) ^ 1);
+            if (!ok) { fail(); break; }
             float* sc = s_scale + ss * C::kScaleFloats + 4 * lane;
 #pragma unroll
             for (int k = 0; k < kWScaleSteps; ++k)
@@ -682,7 +697,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     int t = first;
     bool ok = t < ntiles && decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti);
     if (ok) open(ti);
-    while (ok && !*abort_flag) {
+    while (ok && !warp_aborted(abort_flag)) {
       const int qn = ti.cols;
       uint64_t acc[kWCols / 2];
 #pragma unroll
@@ -697,8 +712,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           pa += a.ldsa;
           if (!ROWS) sb[2] = __ldg(pb++);
         }
-        if ((ROWS && within == 0 && !mbar_wait(&sfull[ss], (sl / kWScaleSlots) & 1)) ||
-            !mbar_wait(&done[it % kWStages], (it / kWStages) & 1)) {
+        if ((ROWS && within == 0 && !warp_wait(&sfull[ss], (sl / kWScaleSlots) & 1)) ||
+            !warp_wait(&done[it % kWStages], (it / kWStages) & 1)) {
           ok = false;
           fail();
           break;
@@ -833,49 +848,76 @@ cudaError_t check_registers(K kern, int threads, int need) {
   return at.numRegs * threads >= need ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
+// Tall form, two CTAs per SM.  A product of few tiles splits K over the CTAs of a
+// cluster: the split, up to 8, with the fewest steps one behind the other.  A
+// step takes nearly twice as long where two CTAs share an SM (they share its
+// loads), a CTA more in the cluster's sum a fifth of a step.  2048 x 8192: M = 128
+// as 4 CTAs a tile 13.9 us, as 8 15.7; M = 256 as 2 21.5, as 4 18.9; 1024 x 1024,
+// M = 8: as 4 6.3, as 8 5.8.  A
+// second wave, whose clusters must find their SMs free together, costs twelve
+// steps more: M = 384 as 5 31.4, as 2 27.9.  The runtime's count of resident clusters (74 of 2,
+// 45 of 3, 33 of 4, 22 of 6, 15 of 8) takes one CTA per SM for kernels that
+// allocate TMEM; the GPU holds two, so beyond the count SMs are shared, and beyond
+// twice the count there is another wave: 80 clusters of 3 overlap (13 us for
+// 16 x 10240 x 8192 in L2).
+constexpr double kSharedStep = 1.95, kSumStep = 0.2, kWaveSteps = 12;
 template <int NT, typename TO>
-cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
+cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStream_t st) {
   using C = TCfg<NT>;
   auto kern = fp8_tall_kernel<NT, TO>;
-  static bool configured[kMaxDevices] = {};
-  if (!configured[dev]) {
-    cudaError_t e = check_registers(kern, C::kThreads, 128 * kTRegsLow + 128 * kTRegsHigh);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(kMaxGroups));
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  Fp8Args a = args_of(g);
-  a.split = split;
-  CUtensorMap am, bm;
-  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, NT) ||
-      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP))
-    return cudaErrorInvalidValue;
+  static std::atomic<int> clusters[kMaxDevices][9];      // resident clusters of each size (0: not asked)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split > 1 ? n_tiles * split : (n_tiles < 2 * sms ? n_tiles : 2 * sms));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::bytes(g.offsets ? g.n_groups : 0);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  if (!clusters[dev][1]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::bytes(kMaxGroups));
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+    for (int c = 8; c >= 1; --c) {
+      at[0].val.clusterDim.x = c;
+      cfg.gridDim = dim3(c * (sms / c));
+      int n = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+      clusters[dev][c] = n > 0 ? n : 1;
+    }
+  }
+  Fp8Args a = args_of(g);
+  if (!g.offsets) {
+    double best = 1e30;
+    for (int c = 1; c <= 8 && c <= a.KB; ++c) {
+      const int held = clusters[dev][c];
+      const double step = n_tiles > held ? kSharedStep : 1.0;
+      const double cost = ceil_div(n_tiles, 2 * held) * (step * ceil_div(a.KB, c) + kSumStep * c + kWaveSteps);
+      if (cost < best) { best = cost; a.split = c; }
+    }
+  }
+  CUtensorMap am, bm;
+  if (!make_tmap_codes(&am, g.a, g.M, g.K, g.lda, NT) ||
+      !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP))
+    return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(a.split > 1 ? n_tiles * a.split : (n_tiles < 2 * sms ? n_tiles : 2 * sms));
+  at[0].val.clusterDim.x = a.split;
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, am, bm, a, n_tiles);
 }
 
 template <int NT>
-cudaError_t tall(const moe_fp8_gemm& g, int n_tiles, int split, int sms, int dev, cudaStream_t st) {
-  return g.out_dtype == MOE_BF16 ? tall_t<NT, __nv_bfloat16>(g, n_tiles, split, sms, dev, st)
-                                 : tall_t<NT, float>(g, n_tiles, split, sms, dev, st);
+cudaError_t tall(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStream_t st) {
+  return g.out_dtype == MOE_BF16 ? tall_t<NT, __nv_bfloat16>(g, n_tiles, sms, dev, st)
+                                 : tall_t<NT, float>(g, n_tiles, sms, dev, st);
 }
 
 template <bool ROWS, typename TO>
 cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStream_t st) {
   using C = WCfg<ROWS>;
   auto kern = fp8_pair_kernel<ROWS, TO>;
-  static int pairs[kMaxDevices] = {};            // co-resident pairs (0: not asked yet)
+  static std::atomic<int> pairs[kMaxDevices];    // co-resident pairs (0: not asked yet)
   if (!pairs[dev]) {
     cudaError_t e = check_registers(kern, kWThreads, 128 * kWRegsLow + 256 * kWRegsHigh);
     if (e == cudaSuccess)
@@ -895,7 +937,7 @@ cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
       !make_tmap_codes(&bm, g.b, (long)a.G * g.N, g.K, g.ldb, kRowsP) ||
       (a.vec && !make_tmap_out(&om, g.out, g.M, g.N, g.ldo, g.out_dtype)))
     return cudaErrorInvalidValue;
-  const int n = n_tiles < pairs[dev] ? n_tiles : pairs[dev];
+  const int room = pairs[dev], n = n_tiles < room ? n_tiles : room;
   kern<<<2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st>>>(am, bm, om, a, n_tiles);
   return cudaGetLastError();
 }
@@ -925,18 +967,26 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
     return n > 0x7fffffff ? 0x7fffffff : (int)n;
   };
   if (g.ldb_scales > 0) return wide<true>(g, tiles(256, 256), sms, dev, st);
-  if (mean > 128) return wide<false>(g, tiles(256, 256), sms, dev, st);
-  const int nt = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-  const int n = tiles(nt, 128);
-  int split = 1;
-  if (!g.offsets)
-    while (split < 8 && split < KB && (long)n * (split + 1) <= 2L * sms) ++split;
-  switch (nt) {
-    case 16: return tall<16>(g, n, split, sms, dev, st);
-    case 32: return tall<32>(g, n, split, sms, dev, st);
-    case 64: return tall<64>(g, n, split, sms, dev, st);
-    default: return tall<128>(g, n, split, sms, dev, st);
+  // Tall or wide.  Up to 64 rows (a group's mean, when grouped) the weights are
+  // what costs, and they are streamed: 64 groups of 5120 x 2048, mean 11 / 44 / 64
+  // / 90 rows: tall 112 / 133 / 176 / 220 us, wide 196 / 199 / 202 / 203.
+  // Plain products of more rows take the form that by its steps is the shorter: a
+  // tall CTA does 0.4 us a step, 0.75 where two share an SM, and 6.5 us besides, most
+  // of them the cluster's sum; a wide pair 0.53 us a step and 4.5.
+  bool use_tall = mean <= 64;
+  if (!use_tall && !g.offsets) {
+    const int nt = tiles(64, 128), nw = tiles(256, 256), pairs = sms / 2;
+    int split = 2 * sms / nt;
+    split = split < 1 ? 1 : split > 8 ? 8 : split;
+    const double step = (long)nt * split > sms ? 0.75 : 0.4;
+    const double tall_us = 6.5 + step * ceil_div((long)nt * split, 2 * sms) * ceil_div(KB, split);
+    const double wide_us = 4.5 + 0.53 * ceil_div(nw, pairs) * KB;
+    use_tall = tall_us < wide_us;
   }
+  if (!use_tall) return wide<false>(g, tiles(256, 256), sms, dev, st);
+  if (mean <= 16) return tall<16>(g, tiles(16, 128), sms, dev, st);
+  if (mean <= 32) return tall<32>(g, tiles(32, 128), sms, dev, st);
+  return tall<64>(g, tiles(64, 128), sms, dev, st);
 }
 
 cudaError_t fp8_gemm_take_error(int* word) {
