@@ -14,8 +14,9 @@
 // Two forms of the tile:
 //   wide  an SM pair's 256 activation rows x 256 weight rows; a thread owns one
 //         activation row, and its scale product is one number for each 128
-//         columns (per column in the weight gradient).  8192 x 10240 x 8192:
-//         650 us, 2.1 PFLOP/s; the clock falls under this load (power), and the
+//         columns (per column in the weight gradient, where it owns four rows and
+//         a quarter of the columns).  8192 x 10240 x 8192:
+//         634 us, 2.2 PFLOP/s; the clock falls under this load (power), and the
 //         promotion's TMEM reads and FMAs share it with the products.
 //   tall  MMA rows = 128 weight rows, MMA columns = 16..64 activation rows: for
 //         few rows, where streaming the weights is the work.  Two CTAs per SM
@@ -87,6 +88,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+// 32 lanes x 64 columns as fragments: thread t gets, for each group i of 8 columns
+// and lane t / 4 + 8 n, columns 8 i + 2 (t % 4) and + 1 in r[n / 2][4 i + 2 (n % 2)]
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[2][32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]), "=r"(r[h][5]),
+          "=r"(r[h][6]), "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]), "=r"(r[h][10]), "=r"(r[h][11]),
+          "=r"(r[h][12]), "=r"(r[h][13]), "=r"(r[h][14]), "=r"(r[h][15]), "=r"(r[h][16]),
+          "=r"(r[h][17]), "=r"(r[h][18]), "=r"(r[h][19]), "=r"(r[h][20]), "=r"(r[h][21]),
+          "=r"(r[h][22]), "=r"(r[h][23]), "=r"(r[h][24]), "=r"(r[h][25]), "=r"(r[h][26]),
+          "=r"(r[h][27]), "=r"(r[h][28]), "=r"(r[h][29]), "=r"(r[h][30]), "=r"(r[h][31])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
 }
 
 // Arrival on a barrier of either CTA of the pair, for hand-overs of TMEM alone:
@@ -481,11 +500,12 @@ constexpr int kWStageBytes = 2 * kPBytes;      // 128 activation rows and 128 we
 static_assert(2 <= kWStages, "two TMEM buffers: a done phase could pass unseen");
 constexpr int kWOutBytes = 32 * 128;           // output staging: 32 rows of 128 bytes
 
-constexpr int kWScaleSteps = 2, kWScaleSlots = 4;    // column scales: steps per slot, slots
+constexpr int kWScaleSlots = 8;                // scale ring: a slot per step
 
 template <bool ROWS>
 struct WCfg {
-  static constexpr int kScaleFloats = ROWS ? kWScaleSteps * kWN : 0;   // column scales of a slot
+  // a slot's scales: of 256 columns and of this CTA's 128 rows
+  static constexpr int kScaleFloats = ROWS ? kWN + kRowsP : 0;
   static constexpr int kOutOffset = kWStages * kWStageBytes;
   static constexpr int kScaleOffset = kOutOffset + kWWarps * 2 * kWOutBytes;
   static constexpr int kBarOffset = kScaleOffset + kWScaleSlots * kScaleFloats * 4;
@@ -502,6 +522,17 @@ __device__ __forceinline__ void mma_pair_f8(uint32_t d, uint64_t ad, uint64_t bd
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate));
+}
+
+// p[i, i + 4), zeros from n on; vec: p is aligned to 16 bytes
+__device__ __forceinline__ float4 four(const float* p, int i, int n, bool vec) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec && i + 4 <= n) return __ldg(reinterpret_cast<const float4*>(p + i));
+  if (i < n) v.x = __ldg(p + i);
+  if (i + 1 < n) v.y = __ldg(p + i + 1);
+  if (i + 2 < n) v.z = __ldg(p + i + 2);
+  if (i + 3 < n) v.w = __ldg(p + i + 3);
+  return v;
 }
 
 // MMA columns of a pair tile: the valid ones rounded up to 32 (each CTA holds half)
@@ -596,42 +627,30 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ---------------- column scales, kWScaleSteps steps at a time (both CTAs) ----------------
+      // ---------------- scales (both CTAs) ----------------
       if constexpr (ROWS) {
-        uint32_t sl = 0;
+        uint32_t it = 0;
         bool ok = true;
-        // whole 16 bytes where the rows of scales allow it
-        const bool vec = a.ldsb % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sb) & 15u) == 0;
         for (int t = first; t < ntiles && ok && !warp_aborted(abort_flag); t += step) {
           Tile ti;
           if (!decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti)) break;
+          const int row0 = (int)rank * kRowsP;
           const float* sb = a.sb + ti.n0;
-          for (int kb = 0; kb < a.KB; kb += kWScaleSteps, ++sl) {
-            const uint32_t ss = sl % kWScaleSlots;
-            float4 v[kWScaleSteps][2];
-#pragma unroll
-            for (int k = 0; k < kWScaleSteps; ++k, sb += a.ldsb)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int i = 4 * lane + 128 * h;
-                v[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (kb + k >= a.KB) continue;
-                if (vec && i + 4 <= ti.cols) {
-                  v[k][h] = __ldg(reinterpret_cast<const float4*>(sb + i));
-                } else {
-                  if (i < ti.cols) v[k][h].x = __ldg(sb + i);
-                  if (i + 1 < ti.cols) v[k][h].y = __ldg(sb + i + 1);
-                  if (i + 2 < ti.cols) v[k][h].z = __ldg(sb + i + 2);
-                  if (i + 3 < ti.cols) v[k][h].w = __ldg(sb + i + 3);
-                }
-              }
-            ok = warp_wait(&sempty[ss], ((sl / kWScaleSlots) & 1) ^ 1);
+          const float* sa = a.sa + ti.m0 + row0;
+          // whole 16 bytes where the rows of scales allow it
+          const bool vec_b = a.ldsb % 4 == 0 && (reinterpret_cast<uintptr_t>(sb) & 15u) == 0;
+          const bool vec_a = a.ldsa % 4 == 0 && (reinterpret_cast<uintptr_t>(sa) & 15u) == 0;
+          for (int kb = 0; kb < a.KB; ++kb, ++it, sb += a.ldsb, sa += a.ldsa) {
+            const uint32_t ss = it % kWScaleSlots;
+            const float4 v0 = four(sb, 4 * lane, ti.cols, vec_b);
+            const float4 v1 = four(sb, 4 * lane + 128, ti.cols, vec_b);
+            const float4 v2 = four(sa, 4 * lane, ti.rows - row0, vec_a);
+            ok = warp_wait(&sempty[ss], ((it / kWScaleSlots) & 1) ^ 1);
             if (!ok) { fail(); break; }
-            float* sc = s_scale + ss * C::kScaleFloats + 4 * lane;
-#pragma unroll
-            for (int k = 0; k < kWScaleSteps; ++k)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) *reinterpret_cast<float4*>(sc + k * kWN + 128 * h) = v[k][h];
+            float4* sc = reinterpret_cast<float4*>(s_scale + ss * C::kScaleFloats) + lane;
+            sc[0] = v0;
+            sc[32] = v1;
+            sc[64] = v2;
             mbar_arrive(&sfull[ss]);
           }
         }
@@ -675,20 +694,27 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
     uint8_t* stage = smem + C::kOutOffset + (warp - 4) * 2 * kWOutBytes;
     TO* out = static_cast<TO*>(a.out);
-    uint32_t it = 0, sl = 0;                               // steps; slots of column scales
-    // scales of this thread's row (times its 128 columns' block scale) are read
-    // three steps ahead; those of the next tile's first steps before this tile
-    // is written out
+    uint32_t it = 0;
+    // Block scales: a thread owns one row; its scale (times its 128 columns' block
+    // scale) is read three steps ahead, the next tile's first ones before this tile
+    // is written out.
+    // Column scales: a thread reads TMEM as 16 x 8 fragments and owns four rows
+    // (lane / 4 + 8 n) and a quarter of the columns, so that it takes 32 column
+    // scales and 4 row scales a step from shared memory, not 128 column scales, whose
+    // broadcasts took 1024 cycles of it (2048 x 8192 x 4096: 160 -> 139 us).  What
+    // bounds this form is two operations an element instead of one, the product of
+    // the scales and the FMA.
     const float *pa = nullptr, *pb = nullptr;
     float sa[3], sb[3];
     auto open = [&](const Tile& ti) {
+      if (ROWS) return;
       const int row = r0 + lane;
       pa = a.sa + ti.m0 + (row < ti.rows ? row : 0);
       pb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128 + (c0 < ti.cols ? half : 0)) * a.KB;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         sa[i] = i < a.KB ? __ldg(pa + (size_t)i * a.ldsa) : 0.f;
-        sb[i] = !ROWS && i < a.KB ? __ldg(pb + i) : 1.f;
+        sb[i] = i < a.KB ? __ldg(pb + i) : 0.f;
       }
       pa += 3 * a.ldsa;
       pb += 3;
@@ -698,57 +724,79 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     bool ok = t < ntiles && decode<2 * kRowsP, kWN>(a, s_tiles, s_off, t, ti);
     if (ok) open(ti);
     while (ok && !warp_aborted(abort_flag)) {
-      const int qn = ti.cols;
+      const int qn = ti.cols, nc = qn - c0;                // columns of this half
       uint64_t acc[kWCols / 2];
 #pragma unroll
       for (int j = 0; j < kWCols / 2; ++j) acc[j] = 0;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
-        const uint32_t ss = sl % kWScaleSlots, b = it & 1;
-        const int within = kb % kWScaleSteps;
-        const float rs = sa[0] * sb[0];
-        sa[0] = sa[1]; sa[1] = sa[2]; sb[0] = sb[1]; sb[1] = sb[2];
-        if (kb + 3 < a.KB) {
-          sa[2] = __ldg(pa);
-          pa += a.ldsa;
-          if (!ROWS) sb[2] = __ldg(pb++);
+        const uint32_t ss = it % kWScaleSlots, b = it & 1;
+        uint64_t rs = 0;
+        if constexpr (!ROWS) {
+          rs = both(sa[0] * sb[0]);
+          sa[0] = sa[1]; sa[1] = sa[2]; sb[0] = sb[1]; sb[1] = sb[2];
+          if (kb + 3 < a.KB) {
+            sa[2] = __ldg(pa);
+            pa += a.ldsa;
+            sb[2] = __ldg(pb++);
+          }
         }
-        if ((ROWS && within == 0 && !warp_wait(&sfull[ss], (sl / kWScaleSlots) & 1)) ||
+        if ((ROWS && !warp_wait(&sfull[ss], (it / kWScaleSlots) & 1)) ||
             !warp_wait(&done[it % kWStages], (it / kWStages) & 1)) {
           ok = false;
           fail();
           break;
         }
         tc_fence_after();
-        const uint64_t rs2 = both(rs);
-        const float* cs = s_scale + ss * C::kScaleFloats + within * kWN + c0;
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_tmem(tempty_leader + b * (uint32_t)sizeof(uint64_t));
+        };
+        const float* cs = s_scale + ss * C::kScaleFloats;
+        uint64_t rr[4];
+        if constexpr (ROWS) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) rr[n] = both(cs[kWN + 32 * q + (lane >> 2) + 8 * n]);
+          cs += c0 + 2 * (lane & 3);
+        }
+        // the buffer is given back once its last columns are read, before they are
+        // added (8192 x 10240 x 8192: 647 -> 634 us)
+        bool held = true;
 #pragma unroll
         for (int c = 0; c < kWCols; c += 64) {
-          if (c0 + c >= qn) break;                         // uniform in the warp
+          if (c >= nc) break;                              // uniform in the warp
           uint32_t r[2][32];
-          pair2::tmem_ld32(tbase + b * kWN + c, r[0]);
-          pair2::tmem_ld32(tbase + b * kWN + c + 32, r[1]);
+          if constexpr (ROWS) {
+            tmem_ld_frag(tbase + b * kWN + c, r);
+          } else {
+            pair2::tmem_ld32(tbase + b * kWN + c, r[0]);
+            pair2::tmem_ld32(tbase + b * kWN + c + 32, r[1]);
+          }
           tmem_ld_wait();
+          if (c + 64 >= kWCols) { release(); held = false; }
+          uint64_t* s = &acc[c >> 1];
+          if constexpr (ROWS) {
+            // s[4 i + n]: columns c + 8 i + 2 (lane % 4) and + 1, row lane / 4 + 8 n
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const uint32_t* p = &r[j >> 5][j & 31];
-            uint64_t* s = &acc[(c + j) >> 1];
-            if constexpr (ROWS) {
-              const uint4 w = *reinterpret_cast<const uint4*>(cs + c + j);
-              s[0] = fma2(pack2(p[0], p[1]), mul2(rs2, pack2(w.x, w.y)), s[0]);
-              s[1] = fma2(pack2(p[2], p[3]), mul2(rs2, pack2(w.z, w.w)), s[1]);
-            } else {
-              s[0] = fma2(pack2(p[0], p[1]), rs2, s[0]);
-              s[1] = fma2(pack2(p[2], p[3]), rs2, s[1]);
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t w = *reinterpret_cast<const uint64_t*>(cs + c + 8 * i);
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const uint32_t* v = &r[n >> 1][4 * i + 2 * (n & 1)];
+                s[4 * i + n] = fma2(pack2(v[0], v[1]), mul2(rr[n], w), s[4 * i + n]);
+              }
             }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 64; j += 2)
+              s[j >> 1] = fma2(pack2(r[j >> 5][j & 31], r[j >> 5][(j & 31) + 1]), rs, s[j >> 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          arrive_tmem(tempty_leader + b * (uint32_t)sizeof(uint64_t));
-          if (ROWS && (within == kWScaleSteps - 1 || kb == a.KB - 1)) mbar_arrive(&sempty[ss]);
+        if (held) release();
+        if (ROWS) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[ss]);
         }
-        if (ROWS && (within == kWScaleSteps - 1 || kb == a.KB - 1)) ++sl;
       }
       if (!ok) break;
       const Tile cur = ti;
@@ -769,18 +817,33 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
         uint8_t* buf = stage + ((c / W) & 1) * kWOutBytes;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // buf's last store
         __syncwarp();
+        if constexpr (ROWS) {
+          const int l = lane >> 2, x = 2 * (lane & 3);     // row of 8, column of 8
+          const uint32_t off = l * 128 + (((x / V) ^ l) << 4) + x % V * sizeof(TO);
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          uint4 v;
-          TO* e = reinterpret_cast<TO*>(&v);
+          for (int i = 0; i < W / 8; ++i)
 #pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            float lo, hi;
-            unpack2(acc[(c + h * V + i) >> 1], lo, hi);
-            if constexpr (sizeof(TO) == 2) *reinterpret_cast<__nv_bfloat162*>(e + i) = __floats2bfloat162_rn(lo, hi);
-            else { e[i] = lo; e[i + 1] = hi; }
+            for (int n = 0; n < 4; ++n) {
+              uint8_t* at = buf + 1024 * n + (off ^ ((8 * i / V) << 4));
+              float lo, hi;
+              unpack2(acc[(c + 8 * i) / 2 + n], lo, hi);
+              if constexpr (sizeof(TO) == 2) *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(lo, hi);
+              else *reinterpret_cast<float2*>(at) = make_float2(lo, hi);
+            }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            uint4 v;
+            TO* e = reinterpret_cast<TO*>(&v);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+              float lo, hi;
+              unpack2(acc[(c + h * V + i) >> 1], lo, hi);
+              if constexpr (sizeof(TO) == 2) *reinterpret_cast<__nv_bfloat162*>(e + i) = __floats2bfloat162_rn(lo, hi);
+              else { e[i] = lo; e[i + 1] = hi; }
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
           }
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((h ^ (lane & 7)) << 4)) = v;
         }
         const bool whole = a.vec && rows >= 32;
         if (whole) fence_proxy_async();
