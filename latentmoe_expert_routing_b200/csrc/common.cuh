@@ -70,4 +70,32 @@ __device__ __forceinline__ float relu2(float v) {
 
 __host__ __device__ inline int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
 
+// Launches that may begin while the stream's last kernel still runs.  A kernel
+// launched so calls after_previous() in every thread before it touches global
+// memory: from there on all that came before it is complete and visible.  (A
+// block that ended without it could end the kernel before the one in front.)
+// A kernel calls let_next() when what is launched behind it may set up (barriers,
+// tensor memory, descriptors) in the shadow of its end; the next one starts when
+// all blocks of this one have, so it takes no room that this one waits for.
+// Three calls of grouping and one of routing 61 -> 53 us at 16384 x 512, a
+// quantisation and a product of 64 rows 34.8 -> 32.8 us.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         A&&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace lmoe

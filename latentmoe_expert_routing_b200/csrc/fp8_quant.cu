@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
 quant_rows_kernel(const QuantArgs a) {
   __shared__ float s_scale[kQBlocks][kQRows + 1];
   const int sub = threadIdx.x & 15, rl = threadIdx.x >> 4;
+  let_next();
+  after_previous();
   const int kb0 = blockIdx.x * kQBlocks, nkb = (a.K + 127) >> 7;
   for (long r0 = (long)blockIdx.y * kQRows; r0 < a.rows; r0 += (long)gridDim.y * kQRows) {
     const long r = r0 + rl;
@@ -214,6 +216,8 @@ quant_cols_kernel(const QuantArgs a) {
   __shared__ float s_max[8][64];
   __shared__ float s_q[64];
   __shared__ __align__(16) uint8_t s_t[64][128 + 16];
+  let_next();
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 64 + 2 * lane;
   const long r0 = (long)blockIdx.y * 128 + 16 * warp;
@@ -289,6 +293,8 @@ __global__ void __launch_bounds__(256)
 quant_square_kernel(const QuantArgs a) {
   __shared__ float s_max[8];
   __shared__ __align__(16) uint8_t s_t[128][128 + 16];
+  let_next();
+  after_previous();
   const int nb = blockIdx.x, kb = blockIdx.y;
   const long mat = blockIdx.z;
   const int NB = (a.rows + 127) >> 7, KB = (a.K + 127) >> 7;
@@ -364,14 +370,15 @@ cudaError_t launch_quantize_fp8_rows(const void* x, moe_dtype dt, int rows, int 
   a.codes = codes; a.ldc = ldc; a.scales = scales; a.lds = lds; a.vec = rows16(x, ldx, dt);
   const int gy = ceil_div(rows, kQRows);
   const dim3 grid(ceil_div(K, 128 * kQBlocks), gy < 65535 ? gy : 65535);
+  cudaError_t e;
   if (dt == MOE_BF16) {
-    if (relu2) quant_rows_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(a);
-    else quant_rows_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(a);
+    if (relu2) e = launch_early(quant_rows_kernel<__nv_bfloat16, true>, grid, 256, 0, st, a);
+    else e = launch_early(quant_rows_kernel<__nv_bfloat16, false>, grid, 256, 0, st, a);
   } else {
-    if (relu2) quant_rows_kernel<float, true><<<grid, 256, 0, st>>>(a);
-    else quant_rows_kernel<float, false><<<grid, 256, 0, st>>>(a);
+    if (relu2) e = launch_early(quant_rows_kernel<float, true>, grid, 256, 0, st, a);
+    else e = launch_early(quant_rows_kernel<float, false>, grid, 256, 0, st, a);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_quantize_fp8_cols(const void* x, moe_dtype dt, int rows, int K, long ldx,
@@ -382,9 +389,10 @@ cudaError_t launch_quantize_fp8_cols(const void* x, moe_dtype dt, int rows, int 
   a.codes = codes; a.ldc = ldc; a.scales = scales; a.lds = lds;
   a.vec = ldx % 2 == 0 && (reinterpret_cast<uintptr_t>(x) & (dt == MOE_BF16 ? 3u : 7u)) == 0;
   const dim3 grid(ceil_div(K, 64), ceil_div(rows, 128));
-  if (dt == MOE_BF16) quant_cols_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  else quant_cols_kernel<float><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaError_t e;
+  if (dt == MOE_BF16) e = launch_early(quant_cols_kernel<__nv_bfloat16>, grid, 256, 0, st, a);
+  else e = launch_early(quant_cols_kernel<float>, grid, 256, 0, st, a);
+  return e;
 }
 
 cudaError_t launch_quantize_fp8_weight(const void* w, moe_dtype dt, int n_mat, int N, int K,
@@ -395,9 +403,10 @@ cudaError_t launch_quantize_fp8_weight(const void* w, moe_dtype dt, int n_mat, i
   a.x = w; a.ldx = ldx; a.rows = N; a.K = K; a.codes = codes; a.ldc = ldc; a.scales = scales;
   a.codes_t = codes_t; a.ldct = ldct; a.scales_t = scales_t; a.vec = rows16(w, ldx, dt);
   const dim3 grid(ceil_div(N, 128), ceil_div(K, 128), n_mat);
-  if (dt == MOE_BF16) quant_square_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  else quant_square_kernel<float><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaError_t e;
+  if (dt == MOE_BF16) e = launch_early(quant_square_kernel<__nv_bfloat16>, grid, 256, 0, st, a);
+  else e = launch_early(quant_square_kernel<float>, grid, 256, 0, st, a);
+  return e;
 }
 
 }  // namespace lmoe

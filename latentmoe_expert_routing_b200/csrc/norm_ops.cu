@@ -134,6 +134,7 @@ template <typename T, int VPT>
 __global__ void __launch_bounds__(512)
 norm_fwd_kernel(const moe_norm_args a) {
   __shared__ float s_red[2][32];
+  let_next();
   const int D = a.D, nv = D / kVec;
   const long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -260,6 +261,7 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
     for (int k = 0; k < n_gate + FULL; ++k)
       bulk_row(s_ring + (size_t)st * stage_bytes + k * row_bytes, source(k, row), row_bytes, &s_full[st]);
   };
+  let_next();
   if (RING && threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) sm100::mbar_init(&s_full[i], 1);
     sm100::fence_mbar_init();
@@ -430,8 +432,10 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
 // strands and then over the strands: 32 columns x 32 strands per block.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-norm_bwd_reduce_kernel(const moe_norm_args a, const float* __restrict__ parts, int nblk) {
+norm_bwd_reduce_kernel(const moe_norm_args a, const float* parts, int nblk) {
   __shared__ float s_a[32][33], s_b[32][33];
+  let_next();
+  after_previous();
   const int c = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
   const size_t plane = (size_t)nblk * a.D;
@@ -522,8 +526,7 @@ cudaError_t bwd_t(const moe_norm_args& a, float* ws, cudaStream_t st) {
   cudaError_t e = a.gate_kind == MOE_GATE_FULL ? bwd_f<T, true>(a, s, ws, st)
                                                : bwd_f<T, false>(a, s, ws, st);
   if (e == cudaSuccess && (a.post_weight || a.pre_weight || a.gate_kind == MOE_GATE_CHANNEL)) {
-    norm_bwd_reduce_kernel<T><<<ceil_div(a.D, 32), 1024, 0, st>>>(a, ws, s.blocks);
-    e = cudaGetLastError();
+    e = launch_early(norm_bwd_reduce_kernel<T>, ceil_div(a.D, 32), 1024, 0, st, a, ws, s.blocks);
   }
   return e;
 }

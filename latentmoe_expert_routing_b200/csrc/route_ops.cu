@@ -264,6 +264,7 @@ route_topk_kernel(const TopkArgs a) {
   extern __shared__ float s_dyn[];
   __shared__ __align__(16) float s_sel[kRows][64];
   __shared__ __align__(16) uint64_t s_key[kRows][32];
+  let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = blockDim.x >> 5;
   float* buf = s_dyn + (size_t)warp * (a.E + 64);          // n_group > 1 only
@@ -614,6 +615,8 @@ __global__ void __launch_bounds__(kPairs)
 group_count_kernel(const GroupArgs a) {
   extern __shared__ int32_t s_hist[];                  // [E]
   for (int e = threadIdx.x; e < a.E; e += kPairs) s_hist[e] = 0;
+  let_next();
+  after_previous();
   __syncthreads();
   const long p = (long)blockIdx.x * kPairs + threadIdx.x;
   if (p < a.P) {
@@ -630,6 +633,8 @@ group_count_kernel(const GroupArgs a) {
 __global__ void __launch_bounds__(256)
 group_scan_kernel(const GroupArgs a) {
   const int lane = threadIdx.x & 31, e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  let_next();
+  after_previous();
   if (e >= a.E) return;
   int32_t* c = a.blk + (size_t)e * a.nblk;
   int run = 0;
@@ -673,6 +678,8 @@ group_place_kernel(const GroupArgs a) {
   __shared__ int s_base[1024], s_warp[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kPairWarps / 2 * a.E; i += kPairs) reinterpret_cast<uint32_t*>(s_cnt)[i] = 0u;
+  let_next();
+  after_previous();
   const int c = threadIdx.x < a.E ? a.counts[threadIdx.x] : 0;
   const int off = block_prefix(c, s_warp);             // (a barrier: s_cnt is cleared)
   if (threadIdx.x < a.E) {
@@ -739,16 +746,13 @@ cudaError_t launch_route_group(const int32_t* idx, long P, int E, int32_t* count
                                cudaStream_t st) {
   const GroupArgs a{idx, P, E, ceil_div(P, kPairs), counts, offsets, perm, pos,
                     static_cast<int32_t*>(ws)};
-  group_count_kernel<<<a.nblk, kPairs, (size_t)E * 4, st>>>(a);
-  group_scan_kernel<<<ceil_div(E, 8), 256, 0, st>>>(a);
+  cudaError_t e = launch_early(group_count_kernel, a.nblk, kPairs, (size_t)E * 4, st, a);
+  if (e == cudaSuccess) e = launch_early(group_scan_kernel, ceil_div(E, 8), 256, 0, st, a);
   const size_t sm = (size_t)E * kPairWarps * 2;               // at most 64 KB
-  if (sm > 48 * 1024 - 4500) {
-    const cudaError_t e = cudaFuncSetAttribute(group_place_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-    if (e != cudaSuccess) return e;
-  }
-  group_place_kernel<<<a.nblk, kPairs, sm, st>>>(a);
-  return cudaGetLastError();
+  if (e == cudaSuccess && sm > 48 * 1024 - 4500)
+    e = cudaFuncSetAttribute(group_place_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+  return e == cudaSuccess ? launch_early(group_place_kernel, a.nblk, kPairs, sm, st, a) : e;
 }
 
 cudaError_t route_group_take_error(int* word) {

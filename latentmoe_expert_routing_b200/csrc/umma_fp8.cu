@@ -281,6 +281,8 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     tma_prefetch_desc(&bmap);
   }
   if (warp == 1) { tmem_alloc(tmem_slot, C::kTmemCols); tmem_relinquish(); }
+  let_next();
+  after_previous();
   load_groups<NT, kRowsP>(a, s_tiles, s_off);
   tc_fence_before();
   __syncthreads();
@@ -574,6 +576,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     tma_prefetch_desc(&bmap);
   }
   if (warp == 1) { pair2::tmem_alloc_pair(tmem_slot, 512); pair2::tmem_relinquish_pair(); }
+  let_next();
+  after_previous();
   load_groups<2 * kRowsP, kWN>(a, s_tiles, s_off);
   tc_fence_before();
   __syncthreads();
@@ -933,9 +937,11 @@ cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::bytes(g.offsets ? g.n_groups : 0);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   if (!clusters[dev][1]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -966,7 +972,8 @@ cudaError_t tall_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
     return cudaErrorInvalidValue;
   cfg.gridDim = dim3(a.split > 1 ? n_tiles * a.split : (n_tiles < 2 * sms ? n_tiles : 2 * sms));
   at[0].val.clusterDim.x = a.split;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  cfg.attrs = a.split > 1 ? at : at + 1;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, am, bm, a, n_tiles);
 }
 
@@ -1001,8 +1008,7 @@ cudaError_t wide_t(const moe_fp8_gemm& g, int n_tiles, int sms, int dev, cudaStr
       (a.vec && !make_tmap_out(&om, g.out, g.M, g.N, g.ldo, g.out_dtype)))
     return cudaErrorInvalidValue;
   const int room = pairs[dev], n = n_tiles < room ? n_tiles : room;
-  kern<<<2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st>>>(am, bm, om, a, n_tiles);
-  return cudaGetLastError();
+  return launch_early(kern, 2 * n, kWThreads, C::bytes(g.offsets ? g.n_groups : 0), st, am, bm, om, a, n_tiles);
 }
 
 template <bool ROWS>
