@@ -249,12 +249,6 @@ void launch_gather_rows_f16(const void* z, const int32_t* perm, void* zp, long P
 cudaError_t launch_pow2_scale(const void* z, long n, unsigned* amax, float* mul2, cudaStream_t st);
 void launch_gather_rows(const void* z, const int32_t* perm, void* zp, long P, int k, int L,
                         cudaStream_t st);
-// 8-bit codes [rows][K], rows of `pitch` bytes (a multiple of 16), 128-byte x
-// box_rows boxes, 128-byte swizzle
-bool make_tmap_codes(CUtensorMap* map, const void* base, long rows, int K, long pitch,
-                     int box_rows);
-// fp32 / bf16 output matrix, rows ld elements apart, 32-row x 128-byte boxes, swizzled
-bool make_tmap_out(CUtensorMap* map, void* base, long rows, int cols, long ld, moe_dtype dt);
 }  // namespace lmoe
 
 // Stand-alone operators (ops_api.cu checks the arguments)

@@ -890,6 +890,48 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled, from the driver that is loaded
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// a matrix of `rows` rows, `pitch` bytes apart (a multiple of 16), by boxes of
+// box_rows x 128 bytes in the 128-byte swizzle
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long rows, int cols,
+            long pitch, int es, int box_rows, CUtensorMapL2promotion l2) {
+  const EncodeFn fn = encoder();
+  if (!fn || !base || rows <= 0 || cols <= 0 || pitch < (long)cols * es || pitch % 16) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 8-bit codes: those past a row's K read as zeros
+bool make_tmap_codes(CUtensorMap* map, const void* base, long rows, int K, long pitch, int box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, K, pitch, 1, box_rows,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// the output matrix, rows `ld` elements apart
+bool make_tmap_out(CUtensorMap* map, void* base, long rows, int cols, long ld, moe_dtype dt) {
+  const bool half = dt == MOE_BF16;
+  const int es = half ? 2 : 4;
+  return encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base,
+                rows, cols, ld * es, es, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
 constexpr int kMaxDevices = 64;
 
 Fp8Args args_of(const moe_fp8_gemm& g) {

@@ -281,37 +281,6 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, long rows, int row_bytes, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 8-bit codes [rows][K] in rows of `pitch` bytes, box = box_rows x 128 codes,
-// 128-B swizzle; codes past K read as zeros
-bool make_tmap_codes(CUtensorMap* map, const void* base, long rows, int K, long pitch,
-                     int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn || !base || rows <= 0 || K <= 0 || pitch < K || (pitch % 16)) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)pitch};
-  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// output matrix [rows][cols] of fp32 or bf16, rows `ld` elements apart (a
-// multiple of 16 bytes), box = 32 rows x 128 bytes, 128-B swizzle
-bool make_tmap_out(CUtensorMap* map, void* base, long rows, int cols, long ld, moe_dtype dt) {
-  EncodeTiledFn fn = encode_fn();
-  const int es = dt == MOE_BF16 ? 2 : 4;
-  if (!fn || !base || rows <= 0 || cols <= 0 || ld < cols || (ld * es) % 16) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
-  cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-            base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_tmap_records(CUtensorMap* map, const void* base, long n_records, int batch) {
   EncodeTiledFn fn = encode_fn();
   if (!fn || !base || n_records <= 0 || batch < 1 || batch > 4) return false;
