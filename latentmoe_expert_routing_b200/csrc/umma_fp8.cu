@@ -23,12 +23,12 @@
 //         keep more loads in flight; when the tiles cannot fill the GPU, K is
 //         split over the CTAs of a cluster, which add their sums in rank order
 //         through distributed shared memory (no atomics: one order).
-//         64 x 10240 x 8192 with cold weights: 24.6 us, 3.4 TB/s.
+//         64 x 10240 x 8192 with cold weights: 21.4 us, 4.0 TB/s; 8 rows 17.2, 4.9.
 //
 // Roles: a producer thread (TMA tiles), a warp that lays scale products into a
 // ring of their own (the promotion reads them after the tile's stage is free
 // again; the wide form's row scales are read by the promoting threads), two MMA
-// threads, 4 or 8 promoting warps.  Every wait is bounded; one that runs out sets
+// threads, 4 (tall) or 8 promoting warps.  Every wait is bounded; one that runs out sets
 // DEV_ERR_TIMEOUT, and its whole warp unwinds.
 #include <cuda.h>
 
@@ -139,10 +139,8 @@ struct TCfg {
   static constexpr int kStages = NT <= 32 ? 5 : 4;              // two CTAs share an SM: its shared
   static constexpr int kBufs = 4;                               // memory, and its 512 TMEM columns,
   static constexpr int kSlots = 3;                              // for the partial sums
-  static constexpr int kWarps = NT == 64 ? 8 : 4;               // promoting warps
-  static constexpr int kCols = NT * 4 / kWarps;                 // columns per promoting thread
-  static constexpr int kChunk = NT == 32 ? 32 : 16;             // ... read at a time (80 registers
-                                                                // a thread with 12 warps)
+  static constexpr int kWarps = 4;                              // promoting warps (64 rows: eight of
+                                                                // 80 registers were 9 % slower)
   static constexpr int kThreads = 128 + 32 * kWarps;
   static constexpr int kStepFloats = NT;                        // the columns' scale products
   static constexpr uint32_t kTmemCols = kBufs * NT;
@@ -392,8 +390,7 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
   } else {
     // ---------------- promotion and store ----------------
     const int q = warp & 3;                                // TMEM lane quarter
-    const int c0 = ((warp - 4) >> 2) * C::kCols;           // first column
-    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + c0;
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
     const int prow = 32 * q + lane;                        // this thread's weight row
     uint32_t it = 0, sl = 0;
     bool ok = true;
@@ -401,9 +398,9 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     for (int t = first; t < ntiles && ok && !warp_aborted(abort_flag); t += step) {
       Tile ti;
       if (!decode<NT, kRowsP>(a, s_tiles, s_off, t, ti)) break;
-      uint64_t acc[C::kCols / 2];
+      uint64_t acc[NT / 2];
 #pragma unroll
-      for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
+      for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
       for (int kb = kb0; kb < kb1 && ok; kb += kScaleSteps, ++sl) {
         const uint32_t ss = sl % C::kSlots;
         if (!warp_wait(&sfull[ss], (sl / C::kSlots) & 1)) { ok = false; fail(); break; }
@@ -414,14 +411,13 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           if (!warp_wait(&done[st], (it / C::kStages) & 1)) { ok = false; fail(); break; }
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < C::kCols; c += C::kChunk) {
-            uint32_t r[C::kChunk];
-            if constexpr (C::kChunk == 16) tmem_ld16(tbase + b * NT + c, r);
-            else pair2::tmem_ld32(tbase + b * NT + c, r);
+          for (int c = 0; c < NT; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tbase + b * NT + c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < C::kChunk; j += 4) {
-              const uint4 w = *reinterpret_cast<const uint4*>(sc + c0 + c + j);
+            for (int j = 0; j < 16; j += 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(sc + c + j);
               uint64_t* s = &acc[(c + j) >> 1];
               s[0] = fma2(pack2(r[j], r[j + 1]), pack2(w.x, w.y), s[0]);
               s[1] = fma2(pack2(r[j + 2], r[j + 3]), pack2(w.z, w.w), s[1]);
@@ -437,18 +433,17 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       if (split > 1) {
         // this CTA's sums for the cluster: [column][row] over the stages, whose
         // loads have all been consumed (one tile per CTA when split)
-        float* red = reinterpret_cast<float*>(smem) + c0 * kRowsP + prow;
+        float* red = reinterpret_cast<float*>(smem) + prow;
 #pragma unroll
-        for (int j = 0; j < C::kCols; j += 2) unpack2(acc[j >> 1], red[j * kRowsP], red[(j + 1) * kRowsP]);
+        for (int j = 0; j < NT; j += 2) unpack2(acc[j >> 1], red[j * kRowsP], red[(j + 1) * kRowsP]);
       } else if (prow < ti.cols) {
-        TO* o = out + (size_t)(ti.m0 + c0) * a.ldo + ti.n0 + prow;
-        const int rows = ti.rows - c0;
+        TO* o = out + (size_t)ti.m0 * a.ldo + ti.n0 + prow;
 #pragma unroll
-        for (int j = 0; j < C::kCols; j += 2) {
+        for (int j = 0; j < NT; j += 2) {
           float lo, hi;
           unpack2(acc[j >> 1], lo, hi);
-          if (j < rows) store_val(o + (size_t)j * a.ldo, lo);
-          if (j + 1 < rows) store_val(o + (size_t)(j + 1) * a.ldo, hi);
+          if (j < ti.rows) store_val(o + (size_t)j * a.ldo, lo);
+          if (j + 1 < ti.rows) store_val(o + (size_t)(j + 1) * a.ldo, hi);
         }
       }
     }
@@ -1080,7 +1075,8 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
   if (g.ldb_scales > 0) return wide<true>(g, tiles(256, 256), sms, dev, st);
   // Tall or wide.  Up to 64 rows (a group's mean, when grouped) the weights are
   // what costs, and they are streamed: 64 groups of 5120 x 2048, mean 11 / 44 / 64
-  // / 90 rows: tall 112 / 133 / 176 / 220 us, wide 196 / 199 / 202 / 203.
+  // / 90 rows: tall 110 / 122 / 160 / 207 us, wide 196 / 199 / 198 / 200;
+  // 16 of 2048 x 5120: 32 / 35 / 55 / 58, and 53 wide from 64 rows on.
   // Plain products of more rows take the form that by its steps is the shorter: a
   // tall CTA does 0.4 us a step, 0.75 where two share an SM, and 6.5 us besides, most
   // of them the cluster's sum; a wide pair 0.53 us a step and 4.5.
