@@ -362,9 +362,12 @@ norm_bwd_kernel(const moe_norm_args a, float* parts, const int stages) {
       const long next = row + (long)(stages - 1) * gridDim.x;
       if (next < a.T) fetch(next, st ? st - 1 : stages - 1);
     }
-    const float m1 = rr * rr * rr * (s[0] / (float)D);     // d = dr + rr v - m1 r
+    // d = dr + rr v - m1 r.  One factor at a time: a mean of products with y or r
+    // is of the size of its partner over ry, so the first factor brings it back
+    // into range, where ry^3 by itself leaves it from |y| = 1e13 on.
+    const float m1 = rr * (rr * (rr * (s[0] / (float)D)));
     const float dot = s[1] - m1 * s[2];                    // sum d b
-    const float m2 = wpost ? ry * ry * ry * gt * (dot / (float)D) : 0.f;
+    const float m2 = wpost ? gt * (ry * (ry * (ry * (dot / (float)D)))) : 0.f;
     if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0)
       static_cast<float*>(a.dgate)[row] = ry * dot;
     const uint64_t m12 = both(-m1), m22 = both(-m2), ry2 = both(ry), gt2 = both(gt),

@@ -155,6 +155,30 @@ def test_rows_of_zeros_and_an_infinity(ops):
     assert b.dx[[0, 1, 2, 3, 5]].isfinite().all() and b.dy[[0, 1, 2, 3, 5]].isfinite().all()
 
 
+@pytest.mark.parametrize("scale", [1e14, 1e-9])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_large_and_small_rows(ops, dtype, scale):
+    """|y| = 1e14: ry^3 is below fp32's smallest normal number, the gradient is not."""
+    v = _inputs(5, 520, dtype, "channel", True, True, seed=8)
+    v["x"], v["y"] = v["x"] * scale, v["y"] * scale
+    f = _forward(ops, v, 0.5)
+    _check_forward(v, 0.5, f, dtype)
+    _check_backward(v, 0.5, f, _backward(ops, v, 0.5, f), dtype, 5, v["dr"])
+
+
+def test_zero_rows_and_a_tiny_eps(ops):
+    """ry = 1e15 for a row of zeros, whose cube no fp32 holds: dy = d g w ry."""
+    v = _inputs(3, 264, torch.float32, "token", True, False, seed=9)
+    v["y"].zero_()
+    f = ops.norm_residual(v["x"], v["y"], post_weight=v["post"], gate=v["gate"], eps=1e-30, stats=True)
+    b = ops.norm_residual_backward(v["dr"], None, v["y"], f, post_weight=v["post"], gate=v["gate"])
+    assert torch.equal(f.r, v["x"])
+    c = lambda t: t.cpu().double()
+    ref = c(v["dr"]) * c(v["gate"]) * c(v["post"]) * 1e15
+    _within(b.dy, ref, 32 * U * ref.abs(), "dy")
+    assert not b.dgate.any() and not b.dpost_weight.any()
+
+
 def test_against_differences(ops):
     """Directional central differences of the 64-bit function, r kept in fp32:
     its rounding moves h by units of 2^-24 only, which the kernel's own error
