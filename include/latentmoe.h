@@ -442,7 +442,8 @@ moe_status moe_route_group(const int32_t* topk_idx, int T, int top_k, int n_expe
  *   r = residual_scale * x + gate * n                           rounded to dtype
  *   h = r * rr * pre_weight,   rr = 1 / sqrt(mean(r^2) + eps)   (none if NULL)
  * r is the new stream, h the next block's input; h reads r as it is stored.
- * Sums and statistics are fp32.  gate, in dtype:
+ * Sums and statistics are fp32: a row whose squares leave its range (from about
+ * 1.8e19 on) has norm 0.  gate, in dtype:
  *   MOE_GATE_NONE 1;  MOE_GATE_CHANNEL [D];  MOE_GATE_TOKEN one element a row,
  *   stride ldg;  MOE_GATE_FULL [T, D], row stride ldg
  * Rows have D contiguous elements and start at multiples of their stride; every
@@ -531,7 +532,8 @@ moe_status moe_quantize_fp8_weight(const void* w, moe_dtype dtype, int n_mat, in
  *      block (moe_quantize_fp8_weight's); ldb_scales >= N: a second operand of
  *      A's kind, b_scales ceil(K/128) rows of ldb_scales floats
  * Each block of 128 products is summed by the tensor core, then scaled and
- * added in fp32 in the order of the blocks; out is rounded once to out_dtype.
+ * added in fp32 in the order of the blocks (with few rows in up to 8 stretches
+ * of K, whose sums are added in order); out is rounded once to out_dtype.
  * The three products of a linear layer y = x W^T, all sums along K:
  *   y:  A = x, B = W;   dx: A = dy, B = W transposed;
  *   dW: A = dy transposed, B = x transposed (ldb_scales >= N)
