@@ -147,3 +147,30 @@ def test_captured_with_forks_and_copies(lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once(lib):
+    """the tall form (K split over clusters), the wide form and grouped products of
+    two streams beside each other"""
+    ops, B = lib
+    g = torch.Generator(device="cuda").manual_seed(6)
+    n = lambda *s: torch.empty(*s, device="cuda").normal_(generator=g).bfloat16()
+    offsets = torch.tensor([0, 100, 100, 420, 600], dtype=torch.int32, device="cuda")
+    jobs = [(n(64, 4096), ops.quantize_fp8_weight(n(2048, 4096)), None),
+            (n(1500, 1024), ops.quantize_fp8_weight(n(2048, 1024)), None),
+            (n(600, 768), ops.quantize_fp8_weight(n(4, 1024, 768)), offsets),
+            (n(16, 2048), ops.quantize_fp8_weight(n(10240, 2048)), None)]
+    want = [ops.gemm_fp8(ops.quantize_fp8(x), w, offsets=o) for x, w, o in jobs]
+    outs = [[torch.empty_like(t) for t in want] for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(40):
+        for s, out in zip(streams, outs):
+            with torch.cuda.stream(s):
+                j = (i + (s is streams[1])) % 4
+                x, w, o = jobs[j]
+                ops.gemm_fp8(ops.quantize_fp8(x), w, offsets=o, out=out[j])
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    B.moe_sync(None, _stream())
