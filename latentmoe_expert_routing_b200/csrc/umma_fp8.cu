@@ -693,7 +693,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
     uint8_t* stage = smem + C::kOutOffset + (warp - 4) * 2 * kWOutBytes;
     TO* out = static_cast<TO*>(a.out);
-    uint32_t it = 0;
+    uint32_t it = 0, pass = 0;
     // Block scales: a thread owns one row; its scale (times its 128 columns' block
     // scale) is read three steps ahead, the next tile's first ones before this tile
     // is written out.
@@ -807,13 +807,15 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       // whole rows leave by one TMA store, behind which the warp goes on (16-byte
       // stores to 32 rows each held it about 6500 cycles a tile, whole-run
       // stores 4000).  The last rows of a group are stored row by row: what lies
-      // behind them is not this group's.
+      // behind them is not this group's.  The two staging buffers alternate over all
+      // the passes of the kernel: a tile with an odd number of them hands the next
+      // tile the other buffer, whose store is the one waited for.
       constexpr int V = 16 / sizeof(TO), W = 8 * V;        // columns per 16 bytes, per pass
       const int rows = cur.rows - r0;
 #pragma unroll
-      for (int c = 0; c < kWCols; c += W) {
+      for (int c = 0; c < kWCols; c += W, ++pass) {
         if (c0 + c >= qn) break;
-        uint8_t* buf = stage + ((c / W) & 1) * kWOutBytes;
+        uint8_t* buf = stage + (pass & 1) * kWOutBytes;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // buf's last store
         __syncwarp();
         if constexpr (ROWS) {
