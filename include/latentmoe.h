@@ -460,7 +460,8 @@ moe_status moe_route_group(const int32_t* topk_idx, int T, int top_k, int n_expe
  * may be dh), dpost_weight, dpre_weight [D] fp32 (with the weights) and dgate:
  * [D] fp32, [T] fp32 or [T, D] dtype (row stride lddg) by the gate's kind.
  * Sums over rows are taken in a fixed order.  T = 0 writes zero sums.
- * workspace: moe_norm_residual_workspace(T, D) bytes, 16-byte aligned. */
+ * workspace: moe_norm_residual_workspace(T, D) bytes, 16-byte aligned (the query
+ * gives 0 for a T or D that the gradient takes none for or refuses). */
 typedef enum {
   MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3
 } moe_gate;

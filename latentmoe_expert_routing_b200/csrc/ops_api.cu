@@ -141,7 +141,8 @@ moe_status moe_norm_residual(const moe_norm_args* a, void* stream) {
 }
 
 size_t moe_norm_residual_workspace(int T, int D) {
-  return T <= 0 || D <= 0 ? 0 : norm_bwd_workspace(T, D);
+  // nothing for what the gradient refuses (below 8 columns there is no shape at all)
+  return T <= 0 || D <= 0 || D % 8 || D > 16384 ? 0 : norm_bwd_workspace(T, D);
 }
 
 moe_status moe_norm_residual_backward(const moe_norm_args* a, void* workspace,

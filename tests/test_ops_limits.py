@@ -1,0 +1,32 @@
+"""Edges of the stand-alone operators' argument ranges, without a GPU."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def B():
+    from latentmoe_expert_routing_b200 import build
+    build.build()
+    from latentmoe_expert_routing_b200 import binding
+    return binding
+
+
+def test_workspace_queries_answer_every_size(B):
+    """In a process of its own: a query must not end it."""
+    code = ("from latentmoe_expert_routing_b200 import binding as B\n"
+            "big = 2 ** 31 - 1\n"
+            "for T in (-big, -1, 0, 1, 4, big):\n"
+            "    for D in (-big, -1, 0, 1, 4, 7, 8, 12, 64, 16384, 16385, 16392, big):\n"
+            "        n = B.moe_norm_residual_workspace(T, D)\n"
+            "        ok = T > 0 and 0 < D <= 16384 and D % 8 == 0\n"
+            "        assert (n > 0) == ok, (T, D, n)\n"
+            "    for k in (-1, 0, 1, 64, big):\n"
+            "        for E in (-1, 0, 1, 1024, big):\n"
+            "            B.moe_route_group_workspace(T, k, E)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
