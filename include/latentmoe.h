@@ -393,7 +393,8 @@ typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
  *            fp64 and rounded once to fp32
  *   choice = s + bias                          (fp32; selection only)
  *   idx    = top_k eligible experts by (choice descending, expert ascending);
- *            n_group > 1: only the topk_group best groups, as in moe_config
+ *            n_group > 1: only the topk_group best groups, as in moe_config (a
+ *            group with fewer than two eligible experts scores -inf)
  *   w      = s[idx] / (sum s[idx] + 1e-20) * scale     (renorm != 0; the sum in
  *            slot order)  or  s[idx] * scale
  * A logit of -inf or NaN, or a choice score that is -inf or NaN through its

@@ -5,7 +5,8 @@
 //   s_e = 1 / (1 + exp(-l_e))            or   exp(l_e - m) / sum_i exp(l_i - m)
 //   c_e = s_e + b_e                      (both fp32; s evaluated in fp64, rounded once)
 //   groups: E / n_group consecutive experts, scored by the fp32 sum of their two
-//           largest c; the topk_group best stay eligible (ties: lower group)
+//           largest c, -inf without two eligible experts; the topk_group best
+//           stay eligible (ties: lower group)
 //   idx = the k eligible experts of largest c (ties: lower expert)
 //   w_j = s_idx / (sum s_idx + 1e-20) * scale     or   s_idx * scale
 // A logit of -inf or NaN takes its expert out: score 0, never eligible.  Slots
@@ -96,7 +97,9 @@ struct TopkArgs {
 };
 
 // The two largest of each group of G consecutive experts, added: lane g returns
-// the sums of groups g and g + 32.  c goes through shared memory, a group's
+// the sums of groups g and g + 32.  A group without a second eligible expert has
+// -inf, whatever the first is: +inf (by its bias) - inf would be a NaN, which
+// counts neither as better nor as worse than the other groups.  c goes through shared memory, a group's
 // stretch starting G | 1 floats behind the last one's (an odd stride, so lanes
 // reading their own groups meet no bank conflicts).
 template <int EPL>
@@ -118,7 +121,7 @@ __device__ __forceinline__ void group_sums(const float (&c)[EPL], int E, int n_g
         m1 = fmaxf(m1, fminf(m0, v));
         m0 = fmaxf(m0, v);
       }
-    sum[h] = __fadd_rn(m0, m1);
+    sum[h] = m1 > -INFINITY ? __fadd_rn(m0, m1) : -INFINITY;
   }
   __syncwarp();
 }
