@@ -28,7 +28,9 @@
 // Roles: a producer thread (TMA tiles), a warp that lays scale products into a
 // ring of their own (the promotion reads them after the tile's stage is free
 // again; the wide form's row scales are read by the promoting threads), two MMA
-// threads, 4 (tall) or 8 promoting warps.  Every wait is bounded; one that runs out sets
+// threads, 4 (tall) or 8 promoting warps.  Scales are read by ordinary loads: the
+// kernel may start while the one that writes them still runs, so they are not
+// constant for its whole life, which a non-coherent load would ask for.  Every wait is bounded; one that runs out sets
 // DEV_ERR_TIMEOUT, and its whole warp unwinds.
 #include <cuda.h>
 
@@ -343,10 +345,10 @@ fp8_tall_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
 #pragma unroll
           for (int k = 0; k < kScaleSteps; ++k, sa += a.ldsa) {
             const bool in = kb + k < kb1;
-            const float bs = in ? __ldg(sb + kb + k) : 0.f;
+            const float bs = in ? sb[kb + k] : 0.f;
 #pragma unroll
             for (int i = 0; i < PL; ++i)
-              v[k][i] = in && lane + 32 * i < ti.rows ? __ldg(sa + lane + 32 * i) * bs : 0.f;
+              v[k][i] = in && lane + 32 * i < ti.rows ? sa[lane + 32 * i] * bs : 0.f;
           }
           ok = warp_wait(&sempty[ss], ((sl / C::kSlots) & 1) ^ 1);
           if (!ok) { fail(); break; }
@@ -524,11 +526,11 @@ __device__ __forceinline__ void mma_pair_f8(uint32_t d, uint64_t ad, uint64_t bd
 // p[i, i + 4), zeros from n on; vec: p is aligned to 16 bytes
 __device__ __forceinline__ float4 four(const float* p, int i, int n, bool vec) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec && i + 4 <= n) return __ldg(reinterpret_cast<const float4*>(p + i));
-  if (i < n) v.x = __ldg(p + i);
-  if (i + 1 < n) v.y = __ldg(p + i + 1);
-  if (i + 2 < n) v.z = __ldg(p + i + 2);
-  if (i + 3 < n) v.w = __ldg(p + i + 3);
+  if (vec && i + 4 <= n) return *reinterpret_cast<const float4*>(p + i);
+  if (i < n) v.x = p[i];
+  if (i + 1 < n) v.y = p[i + 1];
+  if (i + 2 < n) v.z = p[i + 2];
+  if (i + 3 < n) v.w = p[i + 3];
   return v;
 }
 
@@ -712,8 +714,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       pb = a.sb + ((size_t)ti.grp * a.NB + ti.n0 / 128 + (c0 < ti.cols ? half : 0)) * a.KB;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        sa[i] = i < a.KB ? __ldg(pa + (size_t)i * a.ldsa) : 0.f;
-        sb[i] = i < a.KB ? __ldg(pb + i) : 0.f;
+        sa[i] = i < a.KB ? pa[(size_t)i * a.ldsa] : 0.f;
+        sb[i] = i < a.KB ? pb[i] : 0.f;
       }
       pa += 3 * a.ldsa;
       pb += 3;
@@ -734,9 +736,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
           rs = both(sa[0] * sb[0]);
           sa[0] = sa[1]; sa[1] = sa[2]; sb[0] = sb[1]; sb[1] = sb[2];
           if (kb + 3 < a.KB) {
-            sa[2] = __ldg(pa);
+            sa[2] = *pa;
             pa += a.ldsa;
-            sb[2] = __ldg(pb++);
+            sb[2] = *pb++;
           }
         }
         if ((ROWS && !warp_wait(&sfull[ss], (it / kWScaleSlots) & 1)) ||

@@ -30,3 +30,17 @@ def test_workspace_queries_answer_every_size(B):
             "            B.moe_route_group_workspace(T, k, E)\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+def test_kernels_launched_early_read_with_ordinary_loads():
+    """A kernel that may start while the one in front of it still writes its input
+    must not promise that memory to be constant (non-coherent loads do)."""
+    csrc = os.path.join(ROOT, "latentmoe_expert_routing_b200", "csrc")
+    early = []
+    for name in sorted(os.listdir(csrc)):
+        text = open(os.path.join(csrc, name)).read()
+        if name.endswith(".cu") and "after_previous();" in text:
+            early.append(name)
+            for word in ("__ldg", "__restrict__", "ld.global.nc"):
+                assert word not in text, (name, word)
+    assert {"umma_fp8.cu", "fp8_quant.cu", "route_ops.cu", "norm_ops.cu"} <= set(early)
