@@ -29,3 +29,56 @@ def test_group_of_an_infinite_bias_and_nothing_else(ops, E, G, score):  # noqa: 
     ri, rw, _ = R.route(masked, k, score=score, n_group=G, topk_group=keep)
     assert np.array_equal(idx.cpu().numpy(), ri)
     assert (np.abs(w.cpu().double().numpy() - rw) <= (k + 6) * 2.0 ** -24 * rw).all()
+
+
+def _gradient_by_pairs(l, idx, dw, score, renorm):
+    """(dlogits, the size of what each is made of) in 64 bits.  Every difference
+    u_e - C is the sum over experts i of share_i (u_e - u_i), so that nothing
+    cancels which the gradient's own terms do not; with u* of the largest weight
+    its terms are |u_e - u*|, |u*| times what the weights lack to 1, and the sum
+    of share_i |u_i - u*|."""
+    s, _ = R.scores64(l, score)
+    T, E = s.shape
+    out, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        at = idx[t].cpu().numpy()
+        u, chosen = np.zeros(E), np.zeros(E, bool)
+        u[at], chosen[at] = dw[t].double().numpy(), True
+        p = np.where(chosen, s[t], 0.0)
+        if score == "sigmoid" and not renorm:
+            out[t] = p * u * (1 - p)
+            size[t] = np.abs(out[t])
+            continue
+        S = p.sum() + 1e-20
+        share, rest = (p / S, 1e-20 / S) if renorm else (p, s[t][~chosen].sum())
+        star = u[share.argmax()]
+        d = (share * (u[:, None] - u)).sum(1) + rest * u                 # u_e - C
+        terms = np.abs(u - star) + np.abs(star) * rest + (share * np.abs(u - star)).sum()
+        if score == "sigmoid":
+            out[t], size[t] = share * d * (1 - s[t]), share * terms * (1 - s[t])
+        elif renorm:
+            out[t] = share * d - s[t] * (share * u).sum() * rest
+            size[t] = share * terms + s[t] * (np.abs(star) + (share * np.abs(u - star)).sum()) * rest
+        else:
+            out[t], size[t] = s[t] * d, s[t] * terms
+    return out, size
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(8, 1), (8, 2), (40, 5), (512, 22), (128, 64)])
+def test_gradient_of_peaked_rows(ops, E, k, renorm, score):  # noqa: F811
+    """One expert has nearly all of the weight (up to 1 - 1e-7): the gradient is as
+    exact as its own terms.  A score is off by 2 + 24 units of 2^-24 (expf and its
+    argument, at most 24) and 16 + 6 of its sum and quotient, a weight's sum and
+    quotient add k, a product of three such factors and the sums over the slots 24."""
+    T = 12
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(T, E, generator=g)
+    l[torch.arange(T), torch.randint(E, (T,), generator=g)] += torch.linspace(4, 16, T)
+    dw = torch.randn(T, k, generator=g)
+    idx, w = ops.route_topk(l.cuda(), k, score=score, renorm=renorm)
+    dl = ops.route_topk_backward(l.cuda(), idx, w, dw.cuda(), score=score, renorm=renorm)
+    ref, size = _gradient_by_pairs(l, idx, dw, score, renorm)
+    err = np.abs(dl.cpu().double().numpy() - ref)
+    assert (err <= (128 + 2 * k) * 2.0 ** -24 * size + 1e-37).all(), float((err / (size + 1e-37)).max() * 2 ** 24)
