@@ -545,6 +545,8 @@ moe_status moe_quantize_fp8_weight(const void* w, moe_dtype dtype, int n_mat, in
  * device, ascending, within [0, M] (others are clamped to that).  Rows of out
  * outside every group are not written.
  * out [M, N], row stride ldo >= N.  Codes as moe_quantize_fp8 lays them out.
+ * K is at least 1: where there is nothing to add up (the weight gradient of no
+ * rows), the caller fills out with zeros.
  * A device wait that runs out is reported by moe_sync(NULL, stream) as
  * MOE_ERR_TIMEOUT. */
 typedef struct {

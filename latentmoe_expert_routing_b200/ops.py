@@ -413,7 +413,8 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     """out[m, n] = sum_k A[m, k] B[n, k] for a: Fp8 rows [M, K] and b: Fp8
     weights [N, K], or rows [N, K] (the weight gradient).  With offsets [E + 1]
     int32 and b [E, N, K], rows [offsets[e], offsets[e + 1]) take b's matrix e;
-    rows of `out` in no group keep their contents."""
+    rows of `out` in no group keep their contents.  Without offsets K may be 0 (the
+    weight gradient of a batch without rows): zeros."""
     ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
     if not (isinstance(ac, torch.Tensor) and ac.is_cuda):
         _bad("a.codes must be a cuda tensor")
@@ -443,6 +444,8 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     elif out.shape != (M, N) or out.dtype not in _CODE or out.get_device() != dev or \
             out.stride(1) != 1 and N != 1 or out.stride(0) < N and M > 1:
         _bad("out must be [M, N], fp32 or bf16, rows contiguous, on a's device")
+    if K == 0 and offsets is None:
+        return out.zero_()
     ac, lda = _codes(ac, "a")
     bc, ldb = _codes(bc, "b")
     a_scales, lds = _rows(a_scales)
