@@ -15,6 +15,8 @@
 // mean(q y) needs d, which needs mean(v r).  With b = g w_post y the dot product
 // splits, sum q y = sum (dr + rr v) b - rr^3 mean(v r) sum r b, so one block
 // reduction of three sums serves both means.
+#include <atomic>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels.h"
@@ -502,7 +504,7 @@ BwdShape bwd_shape(const moe_norm_args& a) {
 template <typename T, int VPT, bool FULL, bool RING>
 cudaError_t bwd_v(const moe_norm_args& a, const BwdShape& s, float* ws, cudaStream_t st) {
   auto kern = norm_bwd_kernel<T, VPT, FULL, RING>;
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];        // several threads may call
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -23,3 +23,48 @@ def test_weight_gradient_of_no_rows(ops, out):  # noqa: F811
     g.replay()
     assert got.data_ptr() == big[1:, 5:].data_ptr() and not big[1:131, 5:269].any()
     assert float(big.sum()) == 7.0 * (132 * 300 - 130 * 264)
+
+
+def test_several_threads_at_once(ops):  # noqa: F811
+    """Every operator from four host threads at once, each on a stream of its own,
+    the first calls of their shapes included: the bits of one thread's calls."""
+    import threading
+    g = torch.Generator().manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()
+    T, E, k, D = 300, 64, 4, 1032
+    l, x, y, dr, w3 = n(T, E), n(T, D), n(T, D), n(T, D), n(E, 136, D)
+    wn, gate = n(D), n(T, D)
+
+    def run():
+        idx, w = ops.route_topk(l, k)
+        counts, offsets, perm, pos = ops.route_group(idx, E)
+        dl = ops.route_topk_backward(l, idx, w, w)
+        f = ops.norm_residual(x, y, post_weight=wn, gate=gate, pre_weight=wn, stats=True)
+        b = ops.norm_residual_backward(dr, dr, y, f, post_weight=wn, gate=gate, pre_weight=wn)
+        p = ops.gemm_fp8(ops.quantize_fp8(x, perm=perm, k=k), ops.quantize_fp8_weight(w3), offsets=offsets)
+        q = ops.gemm_fp8(ops.quantize_fp8(y, transpose=True), ops.quantize_fp8(x, transpose=True))
+        return [idx, w, offsets, perm, pos, dl, f.r, f.h, *b, p, q]
+
+    torch.cuda.synchronize()
+    got, errors, start = [None] * 4, [], threading.Barrier(4)
+
+    def work(i):
+        try:
+            start.wait(60)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = run()
+            torch.cuda.current_stream().synchronize()
+        except Exception as e:                    # reported below: a thread's own is lost
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    want = run()
+    for o in got:
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
