@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(32 * kRows)
 route_topk_bwd_kernel(const TopkBwdArgs a) {
   extern __shared__ float s_row[];                     // [kRows][E]: gradients of the chosen experts
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kRows + warp;
+  const long t = (long)blockIdx.x * kRows + warp;      // the last block's may pass 2^31
   if (t >= a.T) return;
   float* g = s_row + (size_t)warp * a.E;
   const TL* row = static_cast<const TL*>(a.logits) + (size_t)t * a.ld;

@@ -82,3 +82,23 @@ def test_gradient_of_peaked_rows(ops, E, k, renorm, score):  # noqa: F811
     ref, size = _gradient_by_pairs(l, idx, dw, score, renorm)
     err = np.abs(dl.cpu().double().numpy() - ref)
     assert (err <= (128 + 2 * k) * 2.0 ** -24 * size + 1e-37).all(), float((err / (size + 1e-37)).max() * 2 ** 24)
+
+
+def test_gradient_of_the_most_rows(ops):  # noqa: F811
+    """2^31 - 1 rows: the last block's warps stand for rows up to 2^31.  One expert,
+    logit 0, weights not renormalised: s (1 - s) dw = 1/4 everywhere."""
+    from latentmoe_expert_routing_b200 import binding as B
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 26 GB")
+    l = torch.zeros(T, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(T, dtype=torch.int32, device="cuda")
+    one = torch.ones(T, device="cuda")
+    dl = torch.zeros(T + 8, dtype=torch.bfloat16, device="cuda")
+    B.moe_route_topk_backward(l.data_ptr(), B.MOE_BF16, 1, idx.data_ptr(), one.data_ptr(), one.data_ptr(), T, 1, 1,
+                              B.MOE_SCORE_SIGMOID, 0, 1.0, dl.data_ptr(), 1, torch.cuda.current_stream().cuda_stream)
+    assert (dl[T:] == 0).all()
+    for part in dl[:T].split(1 << 28):
+        assert bool((part == 0.25).all())
+    del l, idx, one, dl, part
+    torch.cuda.empty_cache()                          # the library allocates beside torch
