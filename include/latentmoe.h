@@ -500,7 +500,9 @@ moe_status moe_norm_residual_backward(const moe_norm_args* args, void* workspace
  *   code = E4M3(v * (448 / amax))   fp32 operations, nearest even, saturating
  * so that value(code) * scale stands for v.  A NaN gives a NaN code; an
  * infinite element makes its whole block NaN.  Elements past the matrix count
- * as zeros in their block and have no codes.
+ * as zeros in their block and have no codes.  MOE_ERR_UNSUPPORTED: K within 1024
+ * of 2^31 (rows), more than 65535 blocks along the rows of x (transpose) or along
+ * K, or more than 65535 matrices (weights).
  * Codes lie in rows of ldc bytes, ldc a multiple of 16, 16-byte aligned (what
  * moe_gemm_fp8 reads); bytes between a row's codes and ldc are not written.
  *

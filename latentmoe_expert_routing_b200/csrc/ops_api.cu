@@ -187,6 +187,7 @@ moe_status moe_quantize_fp8(const void* x, moe_dtype dtype, int x_rows, int K, i
   if ((!x && x_rows > 0) || !aligned(x, bytes_of(dtype)) || !aligned(perm, 4) || !scales ||
       !aligned(scales, 4) || !codes_ok(codes, ldc, K))
     return MOE_ERR_INVALID_ARG;
+  if (K > 0x7fffffff - 1024) return MOE_ERR_UNSUPPORTED;      // a CTA's columns end within 32 bits
   return done(launch_quantize_fp8_rows(x, dtype, rows, K, ldx, perm, k, x_rows, relu2 != 0, codes,
                                        ldc, scales, lds, (cudaStream_t)stream));
 }

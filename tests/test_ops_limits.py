@@ -44,3 +44,15 @@ def test_kernels_launched_early_read_with_ordinary_loads():
             for word in ("__ldg", "__restrict__", "ld.global.nc"):
                 assert word not in text, (name, word)
     assert {"umma_fp8.cu", "fp8_quant.cu", "route_ops.cu", "norm_ops.cu"} <= set(early)
+
+
+def test_sizes_past_the_kernels_index_range_are_refused(B):
+    """Addresses are never dereferenced: each call is refused before a launch."""
+    P, top, unsupported = 4096, 2 ** 31 - 1, 2
+    for K in (top, top - 1023):
+        ld = (K + 15) // 16 * 16
+        assert B.lib.moe_quantize_fp8(P, 1, 1, K, K, None, 1, 1, 0, P, ld, P, 1, None) == unsupported
+    assert B.lib.moe_quantize_fp8_t(P, 1, 65535 * 128 + 1, 8, 8, P, 65536 * 128, P, 8, None) == unsupported
+    assert B.lib.moe_quantize_fp8_weight(P, 1, 65536, 8, 8, 8, P, 16, P, None, 0, None, None) == unsupported
+    K = 65535 * 128 + 1
+    assert B.lib.moe_quantize_fp8_weight(P, 1, 1, 8, K, K, P, K + 15, P, None, 0, None, None) == unsupported
