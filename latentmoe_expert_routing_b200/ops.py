@@ -56,6 +56,7 @@ _device = torch._C._cuda_getDevice
 _set_device = torch.cuda.set_device
 _stream = torch._C._cuda_getCurrentRawStream
 _empty = torch.empty
+_Tensor = torch.Tensor
 _F32, _BF16, _I32, _F8, _U8 = (torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn,
                                torch.uint8)
 _CODE = {_F32: B.MOE_FP32, _BF16: B.MOE_BF16}
@@ -82,7 +83,7 @@ def _bad(what):
 
 def _input(t, what, dims=2):
     """The device index and dtype code of a cuda fp32 / bf16 matrix."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+    if not (isinstance(t, _Tensor) and t.is_cuda):
         _bad(f"{what} must be a cuda tensor")
     if t.dim() != dims:
         _bad(f"{what} must have {dims} dimensions")
@@ -93,7 +94,7 @@ def _input(t, what, dims=2):
 
 
 def _like(t, what, dev, dtype, shape):
-    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
         _bad(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
 
 
@@ -139,6 +140,8 @@ def route_topk(logits, k, *, bias=None, score="sigmoid", n_group=1, topk_group=1
     dev, dt = _input(logits, "logits")
     if score not in B.SCORE:
         _bad(f"score must be one of {sorted(B.SCORE)}")
+    if k < 0:
+        _bad("k must not be negative")
     if dev != _device():
         with _on(dev):
             return route_topk(logits, k, bias=bias, score=score, n_group=n_group,
@@ -166,7 +169,7 @@ def route_topk_backward(logits, idx, w, dw, *, score="sigmoid", renorm=True, sca
         with _on(dev):
             return route_topk_backward(logits, idx, w, dw, score=score, renorm=renorm, scale=scale)
     T, E = logits.shape
-    if idx.dim() != 2:
+    if not isinstance(idx, _Tensor) or idx.dim() != 2:
         _bad("idx must be [T, k]")
     k = idx.shape[1]
     _like(idx, "idx", dev, _I32, (T, k))
@@ -184,10 +187,12 @@ def route_topk_backward(logits, idx, w, dw, *, score="sigmoid", renorm=True, sca
 def route_group(idx, n_experts):
     """The pairs t*k + j of idx [T, k] by expert: (counts [E], offsets [E + 1],
     perm [T*k], pos [T*k]), int32, views of one buffer (moe_route_group)."""
-    if not (isinstance(idx, torch.Tensor) and idx.is_cuda):
+    if not (isinstance(idx, _Tensor) and idx.is_cuda):
         _bad("idx must be a cuda tensor")
     if idx.dim() != 2 or idx.dtype != _I32:
         _bad("idx must be int32 [T, k]")
+    if n_experts < 0:
+        _bad("n_experts must not be negative")
     dev = idx.get_device()
     if dev != _device():
         with _on(dev):
@@ -213,6 +218,8 @@ def route_group(idx, n_experts):
 def _gate_kind(gate, T, D):
     if gate is None:
         return B.MOE_GATE_NONE
+    if not isinstance(gate, _Tensor):
+        _bad("gate must be a tensor")
     if gate.shape == (D,):
         return B.MOE_GATE_CHANNEL
     if gate.shape == (T, D) and D > 1:
@@ -226,7 +233,7 @@ def _norm_inputs(T, D, r, y, post_weight, gate, pre_weight):
     """(kind, y, ldy, post_weight, pre_weight, gate, ldg) as the library reads
     them: checked against r's shape, type and device, copied where unaligned."""
     dev, dtype = r.get_device(), r.dtype
-    if y.shape != r.shape or y.dtype != dtype or y.get_device() != dev:
+    if not isinstance(y, _Tensor) or y.shape != r.shape or y.dtype != dtype or y.get_device() != dev:
         _bad("y must have x's shape, type and device")
     y, ldy = _rows16(y)
     if post_weight is not None:
@@ -284,7 +291,10 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
     from dr (None for zero) and dh (with pre_weight): dx, dy in their type,
     dpost_weight, dpre_weight fp32 [D], dgate fp32 [D] / [T, 1] or [T, D] in the
     gate's type."""
-    r, _, ry, rr = forward
+    try:
+        r, _, ry, rr = forward
+    except (TypeError, ValueError):
+        _bad("forward must be what norm_residual returned")
     dev, dt = _input(r, "forward.r")
     if (dh is not None) != (pre_weight is not None):
         _bad("dh goes with pre_weight")
@@ -296,7 +306,7 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
                                           residual_scale=residual_scale, pre_weight=pre_weight)
     T, D = r.shape
     where, dtype = r.device, r.dtype
-    shape = None if gate is None else gate.shape
+    shape = getattr(gate, "shape", None)
     kind, y, ldy, post, pre, gate, ldg = _norm_inputs(T, D, r, y, post_weight, gate, pre_weight)
     r, ldr = _rows16(r)
     lddr = lddh = 0
@@ -359,7 +369,7 @@ def quantize_fp8(x, *, perm=None, k=1, relu2=False, transpose=False):
         return Fp8(codes if ldc == M else codes[:, :M], scales)
     R, at = M, None
     if perm is not None:
-        if perm.dim() != 1 or perm.dtype != _I32 or perm.get_device() != dev:
+        if not isinstance(perm, _Tensor) or perm.dim() != 1 or perm.dtype != _I32 or perm.get_device() != dev:
             _bad("perm must be int32 [R] on x's device")
         perm = perm.contiguous()
         R, at = perm.shape[0], perm.data_ptr()
@@ -374,7 +384,7 @@ def quantize_fp8(x, *, perm=None, k=1, relu2=False, transpose=False):
 def quantize_fp8_weight(w, *, transposed=False):
     """w [N, K] or [E, N, K] with a scale for each 128 x 128 block; with
     `transposed` also the transpose (of each matrix): (Fp8, Fp8)."""
-    dev, dt = _input(w, "w", 3 if isinstance(w, torch.Tensor) and w.dim() == 3 else 2)
+    dev, dt = _input(w, "w", 3 if isinstance(w, _Tensor) and w.dim() == 3 else 2)
     if dev != _device():
         with _on(dev):
             return quantize_fp8_weight(w, transposed=transposed)
@@ -415,14 +425,17 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     int32 and b [E, N, K], rows [offsets[e], offsets[e + 1]) take b's matrix e;
     rows of `out` in no group keep their contents.  Without offsets K may be 0 (the
     weight gradient of a batch without rows): zeros."""
-    ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
-    if not (isinstance(ac, torch.Tensor) and ac.is_cuda):
+    try:
+        ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
+    except AttributeError:
+        _bad("a and b must be Fp8")
+    if not (isinstance(ac, _Tensor) and ac.is_cuda):
         _bad("a.codes must be a cuda tensor")
     dev = ac.get_device()
     if dev != _device():
         with _on(dev):
             return gemm_fp8(a, b, offsets=offsets, out_dtype=out_dtype, out=out)
-    if ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3):
+    if not isinstance(bc, _Tensor) or ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3):
         _bad("a.codes must be [M, K] and b.codes [N, K], or [E, N, K] with offsets")
     M, K = ac.shape
     N = bc.shape[-2]
@@ -430,7 +443,7 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
         _bad("b.codes must have a.codes' K and device")
     KB = _blocks(K)
     _like(a_scales, "a.scales", dev, _F32, (KB, M))
-    if b_scales.dtype != _F32 or b_scales.get_device() != dev:
+    if not isinstance(b_scales, _Tensor) or b_scales.dtype != _F32 or b_scales.get_device() != dev:
         _bad("b.scales must be fp32 on a's device")
     # [NB, KB] and [KB, N] agree only at N = 1, K <= 128, where both are the one scale
     weights = b_scales.shape == (*bc.shape[:-2], _blocks(N), KB)
@@ -441,7 +454,7 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
         if dtype is None:
             _bad(f"out_dtype must be one of {sorted(_OUT)}")
         out = _empty(M, N, dtype=dtype, device=ac.device)
-    elif out.shape != (M, N) or out.dtype not in _CODE or out.get_device() != dev or \
+    elif not isinstance(out, _Tensor) or out.shape != (M, N) or out.dtype not in _CODE or out.get_device() != dev or \
             out.stride(1) != 1 and N != 1 or out.stride(0) < N and M > 1:
         _bad("out must be [M, N], fp32 or bf16, rows contiguous, on a's device")
     if K == 0 and offsets is None:

@@ -68,3 +68,32 @@ def test_several_threads_at_once(ops):  # noqa: F811
     want = run()
     for o in got:
         assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_what_is_no_tensor_raises_value_error(ops):  # noqa: F811
+    """As the module says of wrong arguments, whichever argument it is."""
+    l, x = torch.randn(4, 16).cuda(), torch.randn(4, 64).cuda()
+    idx, w = ops.route_topk(l, 3)
+    f, q, m = ops.norm_residual(x, x, stats=True), ops.quantize_fp8(x), ops.quantize_fp8_weight(x)
+    m3 = ops.Fp8(m.codes[None], m.scales[None])
+    bad = dict(
+        logits=lambda: ops.route_topk([[0.0]], 1), k=lambda: ops.route_topk(l, -1),
+        bias=lambda: ops.route_topk(l, 3, bias=[0.0] * 16), score=lambda: ops.route_topk(l, 3, score="relu"),
+        idx=lambda: ops.route_topk_backward(l, None, w, w), w=lambda: ops.route_topk_backward(l, idx, 1.0, w),
+        dw=lambda: ops.route_topk_backward(l, idx, w, None), group=lambda: ops.route_group(None, 4),
+        n_experts=lambda: ops.route_group(idx, -1), x=lambda: ops.norm_residual(None, x),
+        y=lambda: ops.norm_residual(x, None), post=lambda: ops.norm_residual(x, x, post_weight=1.0),
+        gate=lambda: ops.norm_residual(x, x, gate=0.5), dr=lambda: ops.norm_residual_backward(3, None, x, f),
+        y_backward=lambda: ops.norm_residual_backward(x, None, None, f),
+        gate_backward=lambda: ops.norm_residual_backward(x, None, x, f, gate=0.5),
+        forward=lambda: ops.norm_residual_backward(x, None, x, None),
+        parts=lambda: ops.norm_residual_backward(x, None, x, (x, None)),
+        rows=lambda: ops.quantize_fp8(None), perm=lambda: ops.quantize_fp8(x, perm=[0, 1]),
+        weight=lambda: ops.quantize_fp8_weight(2.0), a=lambda: ops.gemm_fp8(None, m), b=lambda: ops.gemm_fp8(q, x),
+        a_codes=lambda: ops.gemm_fp8(ops.Fp8(None, q.scales), m), b_codes=lambda: ops.gemm_fp8(q, ops.Fp8(None, m.scales)),
+        a_scales=lambda: ops.gemm_fp8(ops.Fp8(q.codes, None), m), b_scales=lambda: ops.gemm_fp8(q, ops.Fp8(m.codes, None)),
+        offsets=lambda: ops.gemm_fp8(q, m3, offsets=[0, 4]), out=lambda: ops.gemm_fp8(q, m, out=3))
+    for name, call in bad.items():
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(name)
