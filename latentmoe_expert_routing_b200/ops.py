@@ -136,7 +136,8 @@ def route_topk(logits, k, *, bias=None, score="sigmoid", n_group=1, topk_group=1
                scale=1.0):
     """Top-k experts and their weights for given router logits [T, E] (fp32 or
     bf16): (idx [T, k] int32, w [T, k] fp32).  bias [E] fp32 enters the selection
-    only; -inf logits take experts out of a row (moe_route_topk)."""
+    only; -inf logits take experts out of a row (moe_route_topk).  w is detached
+    from logits: route_topk_backward is its gradient."""
     dev, dt = _input(logits, "logits")
     if score not in B.SCORE:
         _bad(f"score must be one of {sorted(B.SCORE)}")
@@ -161,7 +162,7 @@ def route_topk(logits, k, *, bias=None, score="sigmoid", n_group=1, topk_group=1
 
 def route_topk_backward(logits, idx, w, dw, *, score="sigmoid", renorm=True, scale=1.0):
     """Gradient of the logits from dw [T, k], given route_topk's arguments and
-    results: dlogits [T, E] in the logits' type."""
+    results: dlogits [T, E] in the logits' type, detached."""
     dev, dt = _input(logits, "logits")
     if score not in B.SCORE:
         _bad(f"score must be one of {sorted(B.SCORE)}")
@@ -264,7 +265,7 @@ def norm_residual(x, y, *, post_weight=None, gate=None, residual_scale=1.0, pre_
     """r = residual_scale * x + gate * norm(y; post_weight) and, with pre_weight,
     h = norm(r; pre_weight), x and y [T, D] fp32 or bf16.  gate: None, [D],
     [T, 1] or [T, D].  stats keeps the reciprocal norms, which
-    norm_residual_backward reads."""
+    norm_residual_backward, the gradient, reads: the results are detached."""
     dev, dt = _input(x, "x")
     if dev != _device():
         with _on(dev):
@@ -290,7 +291,7 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
     """Gradients of norm_residual(.., stats=True), whose result is `forward`,
     from dr (None for zero) and dh (with pre_weight): dx, dy in their type,
     dpost_weight, dpre_weight fp32 [D], dgate fp32 [D] / [T, 1] or [T, D] in the
-    gate's type."""
+    gate's type, all detached."""
     try:
         r, _, ry, rr = forward
     except (TypeError, ValueError):
@@ -350,7 +351,7 @@ def quantize_fp8(x, *, perm=None, k=1, relu2=False, transpose=False):
     """x [M, K] (fp32 or bf16) as E4M3 codes with a scale for each 128 of a row.
     perm [R] int32: row r of the result is row perm[r] // k of x (zeros for an
     entry that names no row).  relu2: of max(x, 0)^2.  transpose: of x's
-    transpose, so codes [K, M]."""
+    transpose, so codes [K, M].  The codes carry no gradient."""
     dev, dt = _input(x, "x")
     if dev != _device():
         with _on(dev):
@@ -383,7 +384,8 @@ def quantize_fp8(x, *, perm=None, k=1, relu2=False, transpose=False):
 
 def quantize_fp8_weight(w, *, transposed=False):
     """w [N, K] or [E, N, K] with a scale for each 128 x 128 block; with
-    `transposed` also the transpose (of each matrix): (Fp8, Fp8)."""
+    `transposed` also the transpose (of each matrix): (Fp8, Fp8).  The codes carry
+    no gradient."""
     dev, dt = _input(w, "w", 3 if isinstance(w, _Tensor) and w.dim() == 3 else 2)
     if dev != _device():
         with _on(dev):
@@ -424,7 +426,8 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     weights [N, K], or rows [N, K] (the weight gradient).  With offsets [E + 1]
     int32 and b [E, N, K], rows [offsets[e], offsets[e + 1]) take b's matrix e;
     rows of `out` in no group keep their contents.  Without offsets K may be 0 (the
-    weight gradient of a batch without rows): zeros."""
+    weight gradient of a batch without rows): zeros.  The result is detached: its gradients are two more
+    products (dx = dy times W's transpose, dW = dy's transpose times x's)."""
     try:
         ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
     except AttributeError:
