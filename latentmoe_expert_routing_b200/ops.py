@@ -11,7 +11,8 @@ Every function runs on the current stream of its tensors' device and returns new
 tensors.  The gradients are calls of their own (route_topk_backward,
 norm_residual_backward, and gemm_fp8 on transposed operands); nothing registers
 with autograd.  Wrong arguments raise ValueError, a refusal by the library
-MoeError.  What the C calls expect and promise stands in include/latentmoe.h.
+MoeError; what kernels find wrong on the device (an expert out of range, a wait
+that ran out) is kept until sync() raises it.  What the C calls expect and promise stands in include/latentmoe.h.
 """
 from __future__ import annotations
 
@@ -127,6 +128,18 @@ def _up16(n):
 
 def _blocks(n):
     return (n + 127) // 128
+
+
+def sync(device=None):
+    """Waits for the current stream of `device` (the current one), then raises
+    MoeError for what the kernels of earlier calls found wrong on that device, and
+    clears it (moe_sync without a handle)."""
+    here = _device()
+    dev = device if isinstance(device, int) else None if device is None else torch.device(device).index
+    if dev is not None and dev != here:
+        with _on(dev):
+            return sync()
+    B.moe_sync(None, _stream(here))
 
 
 # ---------------------------------------------------------------------------
@@ -426,8 +439,9 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
     weights [N, K], or rows [N, K] (the weight gradient).  With offsets [E + 1]
     int32 and b [E, N, K], rows [offsets[e], offsets[e + 1]) take b's matrix e;
     rows of `out` in no group keep their contents.  Without offsets K may be 0 (the
-    weight gradient of a batch without rows): zeros.  The result is detached: its gradients are two more
-    products (dx = dy times W's transpose, dW = dy's transpose times x's)."""
+    weight gradient of a batch without rows): zeros.  The result is detached: its
+    gradients are two more products (dx = dy times W's transpose, dW = dy's
+    transpose times x's)."""
     try:
         ac, bc, a_scales, b_scales = a.codes, b.codes, a.scales, b.scales
     except AttributeError:

@@ -97,3 +97,16 @@ def test_what_is_no_tensor_raises_value_error(ops):  # noqa: F811
         with pytest.raises(ValueError):
             call()
             pytest.fail(name)
+
+
+def test_sync_reports_what_a_kernel_found(ops):  # noqa: F811
+    from latentmoe_expert_routing_b200 import binding as B
+    ops.sync()
+    idx = torch.tensor([[0, 9], [1, 2]], dtype=torch.int32, device="cuda")
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert ops.route_group(idx, 4)[0].tolist() == [1, 1, 1, 0]
+        with pytest.raises(B.MoeError) as e:
+            ops.sync()
+    assert e.value.status == B.MOE_ERR_DEVICE_CHECK
+    for device in (None, 0, "cuda", "cuda:0", torch.device("cuda", 0)):
+        ops.sync(device)                                      # cleared
