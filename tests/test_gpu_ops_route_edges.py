@@ -102,3 +102,31 @@ def test_gradient_of_the_most_rows(ops):  # noqa: F811
         assert bool((part == 0.25).all())
     del l, idx, one, dl, part
     torch.cuda.empty_cache()                          # the library allocates beside torch
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k,G,keep,dtype", [
+    (2100, 64, 6, 1, 1, torch.float32), (2500, 160, 8, 8, 3, torch.float32), (2100, 512, 22, 1, 1, torch.bfloat16),
+    (700, 512, 22, 64, 9, torch.float32), (9500, 24, 3, 1, 1, torch.bfloat16)])
+def test_many_rows(ops, T, E, k, G, keep, dtype, score):  # noqa: F811
+    """Four and eight rows a block, several rows a warp (more than 9472 rows), and
+    lanes that no eligible expert falls to."""
+    g = torch.Generator().manual_seed(T)
+    l = torch.randn(T, E, generator=g).to(dtype).cuda()
+    l[::7, ::4] = NEG
+    b = torch.randn(E, generator=g).mul(0.1).cuda()
+    kw = dict(bias=b, score=score, n_group=G, topk_group=keep, scale=2.5)
+    idx, w = ops.route_topk(l, k, **kw)
+    ri, rw, _ = R.route(l, k, **kw)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert (np.abs(w.cpu().double().numpy() - rw) <= (k + 4) * 2.0 ** -24 * np.abs(rw) + 1e-38).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(9000, 64, 4), (20000, 9, 3), (5000, 512, 22), (3300, 1024, 20)])
+def test_group_of_many_blocks(ops, T, E, k):  # noqa: F811
+    """More than 32 blocks of 1024 pairs: the scan over the blocks takes several
+    steps.  Uneven experts, some without a pair."""
+    g = torch.Generator().manual_seed(T)
+    idx = (torch.rand(T, k, generator=g).pow(3) * (E - 1)).int().cuda()
+    for got, want in zip(ops.route_group(idx, E), R.group(idx.cpu().numpy(), E)):
+        assert np.array_equal(got.cpu().numpy(), want)
