@@ -493,6 +493,7 @@ BwdShape bwd_shape(const moe_norm_args& a) {
   per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
   const int arrays = 1 + (a.pre_weight ? 2 : 0) + (a.dr ? 1 : 0) + (a.gate_kind == MOE_GATE_FULL ? 1 : 0);
   const size_t row = (size_t)arrays * a.D * es, room = size_t(216) << 10;
+  // (777 x 2056 fp32 with a full gate: three blocks an SM leave less than two stages)
   const size_t n = room / per_sm / row;
   s.stages = n < 2 ? 0 : n > kMaxStages ? kMaxStages : (int)n;
   s.smem = row * s.stages;

@@ -16,8 +16,9 @@
 //         activation row, and its scale product is one number for each 128
 //         columns (per column in the weight gradient, where it owns four rows and
 //         a quarter of the columns).  8192 x 10240 x 8192:
-//         634 us, 2.2 PFLOP/s; the clock falls under this load (power), and the
-//         promotion's TMEM reads and FMAs share it with the products.
+//         625 us, 2.2 PFLOP/s, in a short run; under steady load, where the clock
+//         falls (power), 715 to 740 us, 1.9 PFLOP/s, and the promotion's TMEM reads
+//         and FMAs share it with the products.
 //   tall  MMA rows = 128 weight rows, MMA columns = 16..64 activation rows: for
 //         few rows, where streaming the weights is the work.  Two CTAs per SM
 //         keep more loads in flight; when the tiles cannot fill the GPU, K is
@@ -1080,7 +1081,10 @@ cudaError_t launch_fp8_gemm(const moe_fp8_gemm& g, cudaStream_t st) {
   // Tall or wide.  Up to 64 rows (a group's mean, when grouped) the weights are
   // what costs, and they are streamed: 64 groups of 5120 x 2048, mean 11 / 44 / 64
   // / 90 rows: tall 110 / 122 / 160 / 207 us, wide 196 / 199 / 198 / 200;
-  // 16 of 2048 x 5120: 32 / 35 / 55 / 58, and 53 wide from 64 rows on.
+  // 16 of 2048 x 5120: 32 / 35 / 55 / 58, and 53 wide from 64 rows on.  A popular
+  // group among idle ones reads its weights again for each tile of its rows, from
+  // L2: with 90 % of the rows in one of 64 groups, mean 11 / 44 / 90 / 704, 130 /
+  // 172 / 251 / 629 us, where even ones take 109 / 122 / 205 / 556.
   // Plain products of more rows take the form that by its steps is the shorter: a
   // tall CTA does 0.4 us a step, 0.75 where two share an SM, and 6.5 us besides, most
   // of them the cluster's sum; a wide pair 0.53 us a step and 4.5.
