@@ -16,8 +16,8 @@
 //         activation row, and its scale product is one number for each 128
 //         columns (per column in the weight gradient, where it owns four rows and
 //         a quarter of the columns).  8192 x 10240 x 8192:
-//         625 us, 2.2 PFLOP/s, in a short run; under steady load, where the clock
-//         falls (power), 715 to 740 us, 1.9 PFLOP/s, and the promotion's TMEM reads
+//         620 us, 2.2 PFLOP/s, in a short run; under steady load, where the clock
+//         falls (power), about 720 us, 1.9 PFLOP/s, and the promotion's TMEM reads
 //         and FMAs share it with the products.
 //   tall  MMA rows = 128 weight rows, MMA columns = 16..64 activation rows: for
 //         few rows, where streaming the weights is the work.  Two CTAs per SM
@@ -696,7 +696,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
     const int r0 = (int)rank * kRowsP + 32 * q;            // this warp's first row of a tile
     uint8_t* stage = smem + C::kOutOffset + (warp - 4) * 2 * kWOutBytes;
     TO* out = static_cast<TO*>(a.out);
-    uint32_t it = 0, pass = 0;
+    uint32_t it = 0;
     // Block scales: a thread owns one row; its scale (times its 128 columns' block
     // scale) is read three steps ahead, the next tile's first ones before this tile
     // is written out.
@@ -810,16 +810,22 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant_
       // whole rows leave by one TMA store, behind which the warp goes on (16-byte
       // stores to 32 rows each held it about 6500 cycles a tile, whole-run
       // stores 4000).  The last rows of a group are stored row by row: what lies
-      // behind them is not this group's.  The two staging buffers alternate over all
-      // the passes of the kernel: a tile with an odd number of them hands the next
-      // tile the other buffer, whose store is the one waited for.
+      // behind them is not this group's.  The two staging buffers alternate within a
+      // tile; its first pass waits for all earlier stores, since a tile with an odd
+      // number of passes ends on the buffer that the next one begins with.  (A count
+      // of passes over the whole kernel, with no such wait, needs a register through
+      // the main loop and addresses at run time: 8192 x 10240 x 8192 624 us against
+      // 612, the column-scale product 148 against 139.)
       constexpr int V = 16 / sizeof(TO), W = 8 * V;        // columns per 16 bytes, per pass
       const int rows = cur.rows - r0;
 #pragma unroll
-      for (int c = 0; c < kWCols; c += W, ++pass) {
+      for (int c = 0; c < kWCols; c += W) {
         if (c0 + c >= qn) break;
-        uint8_t* buf = stage + (pass & 1) * kWOutBytes;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // buf's last store
+        uint8_t* buf = stage + ((c / W) & 1) * kWOutBytes;
+        if (lane == 0) {                                   // buf's last store has read it
+          if (c == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
         __syncwarp();
         if constexpr (ROWS) {
           const int l = lane >> 2, x = 2 * (lane & 3);     // row of 8, column of 8
