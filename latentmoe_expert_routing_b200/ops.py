@@ -336,24 +336,24 @@ def norm_residual_backward(dr, dh, y, forward, *, post_weight=None, gate=None, r
         _like(rr, "forward.rstd_r", dev, _F32, (T,))
     dx = _empty(T, D, dtype=dtype, device=where)
     dy = _empty(T, D, dtype=dtype, device=where)
-    # the workspace and the column sums in one buffer
+    # the column sums apart from the workspace, which would live as long as they
     need = B.moe_norm_residual_workspace(T, D)
-    ws = (need + 15) // 16 * 4
-    buf = _empty(ws + 3 * D, dtype=_F32, device=where)
-    at, v = buf.data_ptr(), buf.as_strided
-    dpost = None if post is None else v((D,), (1,), ws)
-    dpre = None if pre is None else v((D,), (1,), ws + D)
+    work = _empty(need, dtype=_U8, device=where)
+    sums = _empty(3 * D, dtype=_F32, device=where)
+    at, v = sums.data_ptr(), sums.as_strided
+    dpost = None if post is None else v((D,), (1,), 0)
+    dpre = None if pre is None else v((D,), (1,), D)
     dgate = at_gate = None
     if kind == B.MOE_GATE_CHANNEL:
-        dgate, at_gate = v((D,), (1,), ws + 2 * D), at + 4 * (ws + 2 * D)
+        dgate, at_gate = v((D,), (1,), 2 * D), at + 8 * D
     elif kind:
         dgate = _empty(*shape, dtype=dtype if kind == B.MOE_GATE_FULL else _F32, device=where)
         at_gate = dgate.data_ptr()
     B.moe_norm_residual_backward(B.moe_norm_args(
         T, D, dt, kind, residual_scale, 1.0, None, 0, y.data_ptr(), ldy, _at(post), _at(pre),
         _at(gate), ldg, r.data_ptr(), ldr, None, 0, _at(ry), _at(rr), _at(dr), lddr, _at(dh), lddh,
-        dx.data_ptr(), D, dy.data_ptr(), D, None if post is None else at + 4 * ws,
-        None if pre is None else at + 4 * (ws + D), at_gate, D), at, need, _stream(dev))
+        dx.data_ptr(), D, dy.data_ptr(), D, None if post is None else at,
+        None if pre is None else at + 4 * D, at_gate, D), work.data_ptr(), need, _stream(dev))
     return NormBackward(dx, dy, dpost, dpre, dgate)
 
 

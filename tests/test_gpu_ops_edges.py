@@ -110,3 +110,15 @@ def test_sync_reports_what_a_kernel_found(ops):  # noqa: F811
     assert e.value.status == B.MOE_ERR_DEVICE_CHECK
     for device in (None, 0, "cuda", "cuda:0", torch.device("cuda", 0)):
         ops.sync(device)                                      # cleared
+
+
+def test_weight_gradients_do_not_hold_the_workspace(ops):  # noqa: F811
+    """What a program keeps of a norm's gradient is the column sums, not megabytes
+    of partial ones behind them (nor are they saved with them)."""
+    T, D = 600, 1032
+    n = lambda *s: torch.randn(*s).cuda()
+    x, wn, g = n(T, D), n(D), n(D)
+    f = ops.norm_residual(x, x, post_weight=wn, gate=g, pre_weight=wn, stats=True)
+    b = ops.norm_residual_backward(x, x, x, f, post_weight=wn, gate=g, pre_weight=wn)
+    for t in (b.dpost_weight, b.dpre_weight, b.dgate):
+        assert t.untyped_storage().nbytes() <= 3 * D * 4
