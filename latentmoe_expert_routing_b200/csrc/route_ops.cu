@@ -99,9 +99,9 @@ struct TopkArgs {
 // The two largest of each group of G consecutive experts, added: lane g returns
 // the sums of groups g and g + 32.  A group without a second eligible expert has
 // -inf, whatever the first is: +inf (by its bias) - inf would be a NaN, which
-// counts neither as better nor as worse than the other groups.  c goes through shared memory, a group's
-// stretch starting G | 1 floats behind the last one's (an odd stride, so lanes
-// reading their own groups meet no bank conflicts).
+// counts neither as better nor as worse than the other groups.  c goes through
+// shared memory, a group's stretch starting G | 1 floats behind the last one's (an
+// odd stride, so lanes reading their own groups meet no bank conflicts).
 template <int EPL>
 __device__ __forceinline__ void group_sums(const float (&c)[EPL], int E, int n_group, int lane,
                                            float* buf, float (&sum)[2]) {

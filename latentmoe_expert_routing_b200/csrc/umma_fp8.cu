@@ -31,8 +31,8 @@
 // again; the wide form's row scales are read by the promoting threads), two MMA
 // threads, 4 (tall) or 8 promoting warps.  Scales are read by ordinary loads: the
 // kernel may start while the one that writes them still runs, so they are not
-// constant for its whole life, which a non-coherent load would ask for.  Every wait is bounded; one that runs out sets
-// DEV_ERR_TIMEOUT, and its whole warp unwinds.
+// constant for its whole life, which a non-coherent load would ask for.  Every wait
+// is bounded; one that runs out sets DEV_ERR_TIMEOUT, and its whole warp unwinds.
 #include <cuda.h>
 
 #include <atomic>

@@ -12,7 +12,8 @@ tensors.  The gradients are calls of their own (route_topk_backward,
 norm_residual_backward, and gemm_fp8 on transposed operands); nothing registers
 with autograd.  Wrong arguments raise ValueError, a refusal by the library
 MoeError; what kernels find wrong on the device (an expert out of range, a wait
-that ran out) is kept until sync() raises it.  What the C calls expect and promise stands in include/latentmoe.h.
+that ran out) is kept until sync() raises it.  What the C calls expect and
+promise stands in include/latentmoe.h.
 """
 from __future__ import annotations
 
@@ -471,8 +472,8 @@ def gemm_fp8(a, b, *, offsets=None, out_dtype="bf16", out=None):
         if dtype is None:
             _bad(f"out_dtype must be one of {sorted(_OUT)}")
         out = _empty(M, N, dtype=dtype, device=ac.device)
-    elif not isinstance(out, _Tensor) or out.shape != (M, N) or out.dtype not in _CODE or out.get_device() != dev or \
-            out.stride(1) != 1 and N != 1 or out.stride(0) < N and M > 1:
+    elif not isinstance(out, _Tensor) or out.shape != (M, N) or out.dtype not in _CODE or \
+            out.get_device() != dev or out.stride(1) != 1 and N != 1 or out.stride(0) < N and M > 1:
         _bad("out must be [M, N], fp32 or bf16, rows contiguous, on a's device")
     if K == 0 and offsets is None:
         return out.zero_()
